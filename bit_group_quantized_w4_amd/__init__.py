@@ -102,6 +102,22 @@ SIGNATURES = {
     "w4_dense_linear_f32": (_INT, [_VP, _I64, _I64, _VP, _I64, _VP, _VP]),
     "w4_gptq_block": (_INT, [_VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP]),
     "w4_gptq_block_s16": (_INT, [_VP, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP]),
+    # 8-bit integers with token and channel scales
+    "w4_w8_packed_bytes": (_SZ, [_I64, _I64]),
+    "w4_quantize_w8": (_INT, [_VP, _I64, _I64, _VP, _VP, _VP]),
+    "w4_pack_w8": (_INT, [_VP, _I64, _I64, _VP, _VP]),
+    "w4_unpack_w8": (_INT, [_VP, _I64, _I64, _VP, _VP]),
+    "w4_quantize_tokens": (_INT, [_VP, _I64, _I64, _VP, _VP, _VP]),
+    "w4_quantize_tokens_f32": (_INT, [_VP, _I64, _I64, _VP, _VP, _VP]),
+    "w4_linear_w8a8": (_INT, [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _VP, _VP]),
+    "w4_linear_w8a8_f32": (_INT, [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _VP, _VP]),
+    # rows sorted by expert
+    "w4_linear_grouped": (_INT, [_VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP]),
+    "w4_linear_grouped_s16": (_INT, [_VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP]),
+    "w4_linear_grouped_f32": (_INT, [_VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP]),
+    "w4_linear_grouped_f32_s16": (_INT, [_VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP]),
+    "w4_linear_grouped_w8a8": (_INT, [_VP, _VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP]),
+    "w4_linear_grouped_w8a8_f32": (_INT, [_VP, _VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP]),
 }
 
 
@@ -561,6 +577,219 @@ def dense_linear_f32(x, W, out=None):
     return y
 
 
+# ----------------------------------------------------------------------------
+# 8-bit integers with token and channel scales; rows sorted by expert
+# ----------------------------------------------------------------------------
+
+def _launch(name, device, *args):
+    """Call `name` with the current stream of `device`, made current for the launch
+    (a null stream is the current device's)."""
+    fn = getattr(_lib, name)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(name, device, *args)
+    _check(fn(*args, ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)), name)
+
+
+def _sized(t, dtype, shape, name):
+    """_dev with the shape checked: the kernels take sizes from other arguments."""
+    p = _dev(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    return p
+
+
+def _elements(t, dtype, count, name):
+    p = _dev(t, dtype, name)
+    if t.numel() != count:
+        raise ValueError(f"{name} must hold {count} elements (got {t.numel()})")
+    return p
+
+
+def _matrix(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D (got shape {tuple(t.shape)})")
+    return t.shape
+
+
+def _output(out, out_dtype, M, N, device):
+    """(y, whether it is fp32) of a product's `out` and `out_dtype` arguments."""
+    if out is not None:
+        if not isinstance(out, torch.Tensor):
+            raise TypeError("out must be a torch.Tensor")
+        out_dtype = out.dtype
+    if out_dtype not in OUT_DTYPES:
+        raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+    y = out if out is not None else torch.empty((M, N), dtype=out_dtype, device=device)
+    return y, out_dtype == torch.float32
+
+
+def packed_bytes_w8(N, K):
+    """Bytes of the native 8-bit codes of an N x K matrix (w4_w8_packed_bytes); 0 for a shape
+    the 8-bit functions do not take."""
+    return int(_lib.w4_w8_packed_bytes(N, K))
+
+
+def _bytes_w8(N, K):
+    nb = packed_bytes_w8(N, K)
+    if nb == 0 and N != 0:
+        _check(W4_ERR_SHAPE, "w4_w8_packed_bytes")
+    return nb
+
+
+def quantize_w8(W, out=None):
+    """fp32 weight [N, K] on the GPU -> (codes int8 [packed_bytes_w8(N, K)] in the native layout,
+    scales fp32 [N]): one scale per output channel, codes in [-127, 127].  A stack of experts
+    [E, N, K] gives codes [E, packed_bytes_w8(N, K)] and scales [E, N]."""
+    if not isinstance(W, torch.Tensor) or W.dim() not in (2, 3):
+        raise TypeError("W must be a 2-D (or, for experts, 3-D) torch.Tensor")
+    lead, (N, K) = tuple(W.shape[:-2]), W.shape[-2:]
+    _dev(W, torch.float32, "W")
+    nb = _bytes_w8(N, K)
+    if out is None:
+        out = (torch.empty(lead + (nb,), dtype=torch.int8, device=W.device),
+               torch.empty(lead + (N,), dtype=torch.float32, device=W.device))
+    q, d = out
+    _one_device([W, q, d], "quantize_w8")
+    _sized(q, torch.int8, lead + (nb,), "q"), _sized(d, torch.float32, lead + (N,), "d")
+    for w_, q_, d_ in (zip(W, q, d) if lead else ((W, q, d),)):
+        _launch("w4_quantize_w8", W.device, ctypes.c_void_p(w_.data_ptr()), N, K, ctypes.c_void_p(q_.data_ptr()),
+                ctypes.c_void_p(d_.data_ptr()))
+    return q, d
+
+
+def pack_w8(q_canon, out=None):
+    """Codes int8 [N, K] (computed elsewhere) -> native layout int8 [packed_bytes_w8(N, K)]."""
+    N, K = _matrix(q_canon, "q_canon")
+    nb = _bytes_w8(N, K)
+    q = out if out is not None else torch.empty(nb, dtype=torch.int8, device=q_canon.device)
+    _one_device([q_canon, q], "pack_w8")
+    _launch("w4_pack_w8", q_canon.device, _dev(q_canon, torch.int8, "q_canon"), N, K, _elements(q, torch.int8, nb, "q"))
+    return q
+
+
+def unpack_w8(q, N, K):
+    """Native 8-bit codes -> int8 [N, K]."""
+    p = _elements(q, torch.int8, _bytes_w8(N, K), "q")
+    qc = torch.empty((N, K), dtype=torch.int8, device=q.device)
+    _launch("w4_unpack_w8", q.device, p, N, K, _dev(qc, torch.int8, "q_canon"))
+    return qc
+
+
+def quantize_tokens(x, out=None):
+    """Activations [M, K] (bf16, or fp32) -> (xq int8 [M, K], sx fp32 [M]): one scale per token,
+    codes in [-127, 127].  A token that holds a NaN or an infinity gets scale NaN and codes 0."""
+    M, K = _matrix(x, "x")
+    if x.dtype not in OUT_DTYPES:
+        raise TypeError(f"x must be torch.bfloat16 or torch.float32 (got {x.dtype})")
+    px = _dev(x, x.dtype, "x")
+    if out is None:
+        out = (torch.empty((M, K), dtype=torch.int8, device=x.device),
+               torch.empty(M, dtype=torch.float32, device=x.device))
+    xq, sx = out
+    _one_device([x, xq, sx], "quantize_tokens")
+    _launch("w4_quantize_tokens_f32" if x.dtype == torch.float32 else "w4_quantize_tokens", x.device, px, M, K,
+            _sized(xq, torch.int8, (M, K), "xq"), _sized(sx, torch.float32, (M,), "sx"))
+    return xq, sx
+
+
+def linear_w8a8(xq, sx, q, d, N, out=None, out_dtype=torch.bfloat16):
+    """y [M, N] = (sx x d) * (xq q^T): int8 tokens xq [M, K] with scales sx [M] times native 8-bit
+    weights q with channel scales d [N], summed exactly.  y is bf16, or fp32 with
+    out_dtype=torch.float32 (or an fp32 `out`)."""
+    M, K = _matrix(xq, "xq")
+    p = _dev(xq, torch.int8, "xq")
+    y, f32 = _output(out, out_dtype, M, N, xq.device)
+    _one_device([xq, sx, q, d, y], "linear_w8a8")
+    _launch("w4_linear_w8a8_f32" if f32 else "w4_linear_w8a8", xq.device, p, _sized(sx, torch.float32, (M,), "sx"), M, K,
+            _elements(q, torch.int8, _bytes_w8(N, K), "q"), _sized(d, torch.float32, (N,), "d"), N,
+            _sized(y, y.dtype, (M, N), "out"))
+    return y
+
+
+def _experts(offsets):
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 1:
+        raise TypeError("offsets must be a 1-D torch.Tensor of experts + 1 values")
+    return offsets.numel() - 1
+
+
+def grouped_linear_w8a8(xq, sx, offsets, q, d, N, out=None, out_dtype=torch.bfloat16):
+    """linear_w8a8 with rows sorted by expert: rows offsets[e] .. offsets[e + 1] - 1 of xq use
+    expert e's weight (q [E, packed_bytes_w8(N, K)], d [E, N]; offsets int32 [E + 1] on the GPU).
+    Rows of y that no expert owns are left as they were (undefined without `out`)."""
+    M, K = _matrix(xq, "xq")
+    E = _experts(offsets)
+    p = _dev(xq, torch.int8, "xq")
+    y, f32 = _output(out, out_dtype, M, N, xq.device)
+    _one_device([xq, sx, offsets, q, d, y], "grouped_linear_w8a8")
+    _launch("w4_linear_grouped_w8a8_f32" if f32 else "w4_linear_grouped_w8a8", xq.device, p,
+            _sized(sx, torch.float32, (M,), "sx"), M, K, _dev(offsets, torch.int32, "offsets"), E,
+            _elements(q, torch.int8, E * _bytes_w8(N, K), "q"), _sized(d, torch.float32, (E, N), "d"), N,
+            _sized(y, y.dtype, (M, N), "out"))
+    return y
+
+
+def quantize_rtn_experts(W, scale_dtype=torch.float32):
+    """quantize_rtn of a stack of experts, fp32 [E, N, K] -> (codes uint8 [E, packed_bytes],
+    scales [E, scale_count]), as grouped_linear takes them."""
+    if not isinstance(W, torch.Tensor) or W.dim() != 3:
+        raise TypeError("W must be a 3-D torch.Tensor")
+    if scale_dtype not in SCALE_DTYPES:
+        raise TypeError("scale_dtype must be torch.float32 or torch.bfloat16")
+    _dev(W, torch.float32, "W")
+    E, N, K = W.shape
+    nb, ns = packed_bytes(N, K), scale_count(N, K)
+    if nb == 0 and N != 0:
+        _check(W4_ERR_SHAPE, "packed buffers")
+    q = torch.empty((E, nb), dtype=torch.uint8, device=W.device)
+    d = torch.empty((E, ns), dtype=scale_dtype, device=W.device)
+    name = "w4_quantize_rtn_s16" if scale_dtype == torch.bfloat16 else "w4_quantize_rtn"
+    for w_, q_, d_ in zip(W, q, d):
+        _launch(name, W.device, ctypes.c_void_p(w_.data_ptr()), N, K, ctypes.c_void_p(q_.data_ptr()),
+                ctypes.c_void_p(d_.data_ptr()))
+    return q, d
+
+
+def grouped_linear(x, offsets, q, d, N, out=None, out_dtype=torch.bfloat16):
+    """linear with rows sorted by expert: rows offsets[e] .. offsets[e + 1] - 1 of x (bf16 [M, K])
+    use expert e's 4-bit weight (q uint8 [E, packed_bytes(N, K)], d fp32 or bf16
+    [E, scale_count(N, K)], as quantize_rtn_experts gives them; offsets int32 [E + 1] on the GPU).
+    y [M, N] is bf16, or fp32 with out_dtype=torch.float32 (or an fp32 `out`).  Rows of y that no
+    expert owns are left as they were (undefined without `out`)."""
+    M, K = _matrix(x, "x")
+    E = _experts(offsets)
+    p = _dev(x, torch.bfloat16, "x")
+    sd = _scale_dtype(d)
+    nb, ns = packed_bytes(N, K), scale_count(N, K)
+    if nb == 0 and N != 0:
+        _check(W4_ERR_SHAPE, "packed buffers")
+    y, f32 = _output(out, out_dtype, M, N, x.device)
+    _one_device([x, offsets, q, d, y], "grouped_linear")
+    name = "w4_linear_grouped" + ("_f32" if f32 else "") + ("_s16" if sd == torch.bfloat16 else "")
+    _launch(name, x.device, p, M, K, _dev(offsets, torch.int32, "offsets"), E, _elements(q, torch.uint8, E * nb, "q"),
+            _elements(d, sd, E * ns, "d"), N, _sized(y, y.dtype, (M, N), "out"))
+    return y
+
+
+class W8Linear:
+    """An 8-bit weight held in native layout, callable on bf16 (or fp32) activations: they are
+    quantized token by token and multiplied in int8."""
+
+    def __init__(self, q, d, N, K):
+        self.q, self.d, self.N, self.K = q, d, N, K
+
+    @classmethod
+    def from_float(cls, W):
+        q, d = quantize_w8(W)
+        return cls(q, d, W.shape[0], W.shape[1])
+
+    def __call__(self, x, out=None, out_dtype=torch.bfloat16):
+        xq, sx = quantize_tokens(x)
+        return linear_w8a8(xq, sx, self.q, self.d, self.N, out=out, out_dtype=out_dtype)
+
+
 class W4Linear:
     """A quantized weight held in native layout, callable on bf16 activations."""
 
@@ -578,7 +807,9 @@ class W4Linear:
 
 __all__ = [
     "GROUP", "LIB_PATH", "MAX_BATCH", "OUT_DTYPES", "PATHS", "SCALE_DTYPES", "SIGNATURES", "LinearDesc", "W4Error",
-    "W4Linear", "SplitWorkspace",
+    "W4Linear", "W8Linear", "SplitWorkspace",
+    "grouped_linear", "grouped_linear_w8a8", "linear_w8a8", "pack_w8", "packed_bytes_w8", "quantize_rtn_experts",
+    "quantize_tokens", "quantize_w8", "unpack_w8",
     "awq_scales", "channel_absmean", "library", "linear", "linear_awq", "linear_batched",
     "quantize_rtn_scaled", "scale_activations", "sq_error",
     "pack", "packed_bytes", "quantize_rtn", "scale_count", "unpack",

@@ -211,6 +211,62 @@ w4_status unpack(const uint8_t* q_packed, const void* d_packed, int64_t N, int64
   return hip_status(w4::launch_unpack(q_packed, d_packed, N, K, q_canon, d_canon, s16, stream));
 }
 
+// 8-bit products: 2^14 K stays below 2^31, so no int32 sum overflows whatever
+// the codes are.
+constexpr int64_t kMaxK8 = 130944;
+bool k8_ok(int64_t K) { return k_ok(K) && K <= kMaxK8; }
+// Grouped linears address a tile of up to 256 rows of x with 32-bit offsets.
+constexpr int64_t kMaxKGrouped = int64_t(1) << 20;
+
+w4_status quantize_tokens(const void* x, int64_t M, int64_t K, size_t elem, int8_t* xq, float* sx,
+                          hipStream_t stream) {
+  if (M < 0 || M > kMaxM || !k8_ok(K)) return W4_ERR_SHAPE;
+  if (M == 0) return W4_OK;
+  if (!x || !xq || !sx) return W4_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(xq, 16) || !aligned(sx, 4)) return W4_ERR_ALIGN;
+  const size_t n = (size_t)M * K, sb = 4 * (size_t)M;
+  if (overlaps(xq, n, x, elem * n) || overlaps(sx, sb, x, elem * n) || overlaps(xq, n, sx, sb)) return W4_ERR_ARG;
+  return hip_status(w4::launch_quantize_tokens(x, elem == 4, M, K, xq, sx, stream));
+}
+
+w4_status linear_w8a8(const int8_t* xq, const float* sx, int64_t M, int64_t K, bool grouped, const int32_t* offsets,
+                      int64_t experts, const int8_t* q, const float* d, int64_t N, void* y, size_t out,
+                      hipStream_t stream) {
+  if (M < 0 || M > kMaxM || !n_ok(N) || !k8_ok(K) || experts < 0 || experts > W4_MAX_EXPERTS) return W4_ERR_SHAPE;
+  if (M == 0 || N == 0 || experts == 0) return W4_OK;
+  const size_t qb = w4_w8_packed_bytes(N, K);
+  if (qb >= (size_t)1 << 31) return W4_ERR_SHAPE;  // one matrix is addressed with 32-bit offsets
+  if (!xq || !sx || !q || !d || !y || (grouped && !offsets)) return W4_ERR_NULL;
+  if (!aligned(xq, 16) || !aligned(q, 16) || !aligned(sx, 4) || !aligned(d, 4) || !aligned(y, out) ||
+      !aligned(offsets, 4))
+    return W4_ERR_ALIGN;
+  const size_t yb = out * (size_t)M * N;
+  if (overlaps(y, yb, xq, (size_t)M * K) || overlaps(y, yb, sx, 4 * (size_t)M) ||
+      overlaps(y, yb, q, (size_t)experts * qb) || overlaps(y, yb, d, 4 * (size_t)experts * N) ||
+      (grouped && overlaps(y, yb, offsets, 4 * ((size_t)experts + 1))))
+    return W4_ERR_ARG;
+  return hip_status(w4::launch_linear_w8a8(xq, sx, M, K, grouped ? offsets : nullptr, experts, q, d, N, y, out == 4,
+                                           stream));
+}
+
+w4_status linear_grouped(const uint16_t* x, int64_t M, int64_t K, const int32_t* offsets, int64_t experts,
+                         const uint8_t* q, const void* d, bool s16, int64_t N, void* y, size_t out,
+                         hipStream_t stream) {
+  if (M < 0 || M > kMaxM || !n_ok(N) || !k_ok(K) || K > kMaxKGrouped || experts < 0 || experts > W4_MAX_EXPERTS)
+    return W4_ERR_SHAPE;
+  if (M == 0 || N == 0 || experts == 0) return W4_OK;
+  const size_t qb = w4_packed_bytes(N, K), db = (s16 ? 2 : 4) * w4_scale_count(N, K);
+  if (qb >= (size_t)1 << 31) return W4_ERR_SHAPE;  // one matrix is addressed with 32-bit offsets
+  if (!x || !offsets || !q || !d || !y) return W4_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(offsets, 4) || !aligned(q, 16) || !aligned(d, 16) || !aligned(y, out))
+    return W4_ERR_ALIGN;
+  const size_t yb = out * (size_t)M * N;
+  if (overlaps(y, yb, x, 2 * (size_t)M * K) || overlaps(y, yb, offsets, 4 * ((size_t)experts + 1)) ||
+      overlaps(y, yb, q, (size_t)experts * qb) || overlaps(y, yb, d, (size_t)experts * db))
+    return W4_ERR_ARG;
+  return hip_status(w4::launch_linear_grouped(x, M, K, offsets, experts, q, d, s16, N, y, out == 4, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -844,6 +900,96 @@ w4_status w4_chain_error(const w4_chain_plan* plan, uint32_t* flag, hipStream_t 
   if (hipError_t e = hipStreamSynchronize(stream)) return hip_status(e);
   *flag = v;
   return W4_OK;
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit integers with token and channel scales; rows sorted by expert
+// ---------------------------------------------------------------------------
+size_t w4_w8_packed_bytes(int64_t N, int64_t K) {
+  if (!n_ok(N) || !k8_ok(K)) return 0;
+  return (size_t)padded_rows(N) * (size_t)K;
+}
+
+w4_status w4_quantize_w8(const float* W, int64_t N, int64_t K, int8_t* q_packed, float* d, hipStream_t stream) {
+  if (!n_ok(N) || !k8_ok(K)) return W4_ERR_SHAPE;
+  if (N == 0) return W4_OK;
+  if (!W || !q_packed || !d) return W4_ERR_NULL;
+  if (!aligned(W, 16) || !aligned(q_packed, 16) || !aligned(d, 4)) return W4_ERR_ALIGN;
+  const size_t qb = w4_w8_packed_bytes(N, K), db = 4 * (size_t)N, wb = 4 * (size_t)N * K;
+  if (overlaps(q_packed, qb, d, db) || overlaps(q_packed, qb, W, wb) || overlaps(d, db, W, wb)) return W4_ERR_ARG;
+  return hip_status(w4::launch_quantize_w8(W, N, K, q_packed, d, stream));
+}
+
+w4_status w4_pack_w8(const int8_t* q_canon, int64_t N, int64_t K, int8_t* q_packed, hipStream_t stream) {
+  if (!n_ok(N) || !k8_ok(K)) return W4_ERR_SHAPE;
+  if (N == 0) return W4_OK;
+  if (!q_canon || !q_packed) return W4_ERR_NULL;
+  if (!aligned(q_canon, 16) || !aligned(q_packed, 16)) return W4_ERR_ALIGN;
+  if (overlaps(q_canon, (size_t)N * K, q_packed, w4_w8_packed_bytes(N, K))) return W4_ERR_ARG;
+  return hip_status(w4::launch_pack_w8(q_canon, N, K, q_packed, true, stream));
+}
+
+w4_status w4_unpack_w8(const int8_t* q_packed, int64_t N, int64_t K, int8_t* q_canon, hipStream_t stream) {
+  if (!n_ok(N) || !k8_ok(K)) return W4_ERR_SHAPE;
+  if (N == 0) return W4_OK;
+  if (!q_canon || !q_packed) return W4_ERR_NULL;
+  if (!aligned(q_canon, 16) || !aligned(q_packed, 16)) return W4_ERR_ALIGN;
+  if (overlaps(q_canon, (size_t)N * K, q_packed, w4_w8_packed_bytes(N, K))) return W4_ERR_ARG;
+  return hip_status(w4::launch_pack_w8(q_packed, N, K, q_canon, false, stream));
+}
+
+w4_status w4_quantize_tokens(const uint16_t* x, int64_t M, int64_t K, int8_t* xq, float* sx, hipStream_t stream) {
+  return quantize_tokens(x, M, K, 2, xq, sx, stream);
+}
+
+w4_status w4_quantize_tokens_f32(const float* x, int64_t M, int64_t K, int8_t* xq, float* sx, hipStream_t stream) {
+  return quantize_tokens(x, M, K, 4, xq, sx, stream);
+}
+
+w4_status w4_linear_w8a8(const int8_t* xq, const float* sx, int64_t M, int64_t K, const int8_t* q_packed,
+                         const float* d, int64_t N, uint16_t* y, hipStream_t stream) {
+  return linear_w8a8(xq, sx, M, K, false, nullptr, 1, q_packed, d, N, y, 2, stream);
+}
+
+w4_status w4_linear_w8a8_f32(const int8_t* xq, const float* sx, int64_t M, int64_t K, const int8_t* q_packed,
+                             const float* d, int64_t N, float* y, hipStream_t stream) {
+  return linear_w8a8(xq, sx, M, K, false, nullptr, 1, q_packed, d, N, y, 4, stream);
+}
+
+w4_status w4_linear_grouped_w8a8(const int8_t* xq, const float* sx, int64_t M, int64_t K, const int32_t* offsets,
+                                 int64_t experts, const int8_t* q_packed, const float* d, int64_t N, uint16_t* y,
+                                 hipStream_t stream) {
+  return linear_w8a8(xq, sx, M, K, true, offsets, experts, q_packed, d, N, y, 2, stream);
+}
+
+w4_status w4_linear_grouped_w8a8_f32(const int8_t* xq, const float* sx, int64_t M, int64_t K, const int32_t* offsets,
+                                     int64_t experts, const int8_t* q_packed, const float* d, int64_t N, float* y,
+                                     hipStream_t stream) {
+  return linear_w8a8(xq, sx, M, K, true, offsets, experts, q_packed, d, N, y, 4, stream);
+}
+
+w4_status w4_linear_grouped(const uint16_t* x, int64_t M, int64_t K, const int32_t* offsets, int64_t experts,
+                            const uint8_t* q_packed, const float* d_packed, int64_t N, uint16_t* y,
+                            hipStream_t stream) {
+  return linear_grouped(x, M, K, offsets, experts, q_packed, d_packed, false, N, y, 2, stream);
+}
+
+w4_status w4_linear_grouped_s16(const uint16_t* x, int64_t M, int64_t K, const int32_t* offsets, int64_t experts,
+                                const uint8_t* q_packed, const uint16_t* d_packed, int64_t N, uint16_t* y,
+                                hipStream_t stream) {
+  return linear_grouped(x, M, K, offsets, experts, q_packed, d_packed, true, N, y, 2, stream);
+}
+
+w4_status w4_linear_grouped_f32(const uint16_t* x, int64_t M, int64_t K, const int32_t* offsets, int64_t experts,
+                                const uint8_t* q_packed, const float* d_packed, int64_t N, float* y,
+                                hipStream_t stream) {
+  return linear_grouped(x, M, K, offsets, experts, q_packed, d_packed, false, N, y, 4, stream);
+}
+
+w4_status w4_linear_grouped_f32_s16(const uint16_t* x, int64_t M, int64_t K, const int32_t* offsets, int64_t experts,
+                                    const uint8_t* q_packed, const uint16_t* d_packed, int64_t N, float* y,
+                                    hipStream_t stream) {
+  return linear_grouped(x, M, K, offsets, experts, q_packed, d_packed, true, N, y, 4, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,66 @@
+// Rows sorted by expert: which rows of x, and which expert's weight, a block
+// multiplies.  The row counts are known on the GPU only (`offsets`, experts + 1
+// values), so a launch covers the most row tiles that M rows of that many
+// experts can make -- M / BM full ones and at most one partial one per expert
+// that has rows -- and each block looks its own tile up; blocks past the last
+// tile have nothing to do.
+#pragma once
+
+#include "w4_device.h"
+
+namespace w4 {
+
+struct RowTile {
+  int expert;
+  int r0, r1;  // rows r0 .. r1-1, at most BM of them, at least one
+};
+
+// Row tile `t` of BM rows each: expert by expert, each expert's rows cut from
+// its first one on.  Offsets are clamped to [0, M] and a range that ends before
+// it begins is empty, so whatever the buffer holds no row outside x is named.
+// offsets == nullptr: one expert that has all M rows.  Every lane of the
+// wavefront must call this; the result is the same in all of them.
+__device__ __forceinline__ bool find_row_tile(const int* __restrict__ offsets, int experts, int M, int BM, int t,
+                                              RowTile& o) {
+  if (!offsets) {
+    o.expert = 0;
+    o.r0 = t * BM;
+    o.r1 = min(M, o.r0 + BM);
+    return o.r0 < M;
+  }
+  const int lane = threadIdx.x & 63;
+  int before = 0;  // tiles of the experts before e0
+  for (int e0 = 0; e0 < experts; e0 += 64) {
+    const int e = e0 + lane;
+    int a = 0, b = 0;
+    if (e < experts) {
+      a = min(max(offsets[e], 0), M);
+      b = min(max(offsets[e + 1], 0), M);
+    }
+    const int n = b > a ? (b - a + BM - 1) / BM : 0;
+    int s = n;  // inclusive sum over the lanes
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(s, d);
+      if (lane >= d) s += v;
+    }
+    const uint64_t past = __ballot(before + s > t);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      o.expert = e0 + l;
+      o.r0 = __builtin_amdgcn_readlane(a, l) + (t - before - __builtin_amdgcn_readlane(s - n, l)) * BM;
+      o.r1 = min(__builtin_amdgcn_readlane(b, l), o.r0 + BM);
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(s, 63);
+  }
+  return false;
+}
+
+// Row tiles a launch has to cover (see above).
+inline int64_t max_row_tiles(int64_t M, int64_t experts, bool grouped, int BM) {
+  if (!grouped) return (M + BM - 1) / BM;
+  return M / BM + (experts < M ? experts : M);
+}
+
+}  // namespace w4

@@ -592,6 +592,114 @@ w4_status w4_gptq_block(const float* W, int64_t N, int64_t K, int64_t b0, const 
 w4_status w4_gptq_block_s16(const float* W, int64_t N, int64_t K, int64_t b0, const float* U, int8_t* q_canon,
                             uint16_t* d_canon, float* err, hipStream_t stream);
 
+/*
+ * 8-bit integers with one scale per token and per output channel.  Where the
+ * matrix units rather than the weight stream bound a pass (prefill, many rows
+ * of x), the inputs are quantized too and the product runs in int8:
+ *
+ *   y[m][n] = sx[m] * d[n] * sum_k xq[m][k] q[n][k].
+ *
+ * The equation and rounding are those of the 4-bit codes (study, section 1,
+ * z = 0) with a whole row as the group and 127 as the largest code:
+ *   d  = fl32(max|w| / 127) per row (IEEE divide),
+ *   q  = clamp(round_half_away_from_zero(fl32(w / d)), -127, 127);
+ *   a NaN or infinity in the row gives d = NaN (bits 0x7FC00000) and codes 0;
+ *   d == 0 gives codes 0.
+ * Activations follow the same rule per token: xq and sx in place of q and d.
+ * The int32 sum is exact for every K the functions take; it is rounded to
+ * fp32, multiplied by sx[m] and then by d[n] (one fp32 rounding each: within
+ * 3 * 2^-24 of the exact y, relative) and stored as fp32 or as the nearest-even
+ * bf16 of that value.  This holds while no intermediate leaves the fp32 range:
+ * scales between 2^-60 and 2^48 (or zero) are enough.
+ * A NaN scale makes its whole row (sx) or column (d) of y NaN.
+ *
+ * NATIVE LAYOUT of 8-bit weights: tiles of 16 rows x 64 inputs; tile (r, s)
+ * covers rows 16r .. 16r+15 and inputs 64s .. 64s+63 and is 1024 contiguous
+ * bytes at byte offset (r*(K/64) + s)*1024.  Its 16-byte lane L (0..63) holds
+ * row 16r + (L % 16), inputs 64s + 16(L / 16) .. + 15 in order.  Rows N .. of
+ * the last tiles are zeros.  Scales are fp32 [N], not padded.
+ * Tokens stay row-major: xq int8 [M][K], sx fp32 [M].
+ *
+ * K is a positive multiple of 128, at most 130944, in all of them.
+ */
+
+/* Bytes of native 8-bit codes of an N x K matrix: roundup(N, 16) * K (0 on a
+ * bad shape). */
+size_t w4_w8_packed_bytes(int64_t N, int64_t K);
+
+/* W fp32 [N][K] (16-byte aligned) -> q_packed (w4_w8_packed_bytes(N, K) bytes,
+ * native layout, 16-byte aligned) and d fp32 [N] (4-byte aligned).  Codes and
+ * scales are bit-exact with respect to the conventions above.  The buffers
+ * may not overlap.  N == 0 does nothing. */
+w4_status w4_quantize_w8(const float* W, int64_t N, int64_t K, int8_t* q_packed, float* d, hipStream_t stream);
+
+/* Codes int8 [N][K] row-major (any value, -128 included) <-> native layout;
+ * both 16-byte aligned and disjoint. */
+w4_status w4_pack_w8(const int8_t* q_canon, int64_t N, int64_t K, int8_t* q_packed, hipStream_t stream);
+w4_status w4_unpack_w8(const int8_t* q_packed, int64_t N, int64_t K, int8_t* q_canon, hipStream_t stream);
+
+/* x bf16 (or fp32) [M][K] -> xq int8 [M][K] and sx fp32 [M]; x and xq 16-byte,
+ * sx 4-byte aligned, disjoint.  0 <= M <= 262140 (M == 0: nothing is done). */
+w4_status w4_quantize_tokens(const uint16_t* x, int64_t M, int64_t K, int8_t* xq, float* sx, hipStream_t stream);
+w4_status w4_quantize_tokens_f32(const float* x, int64_t M, int64_t K, int8_t* xq, float* sx, hipStream_t stream);
+
+/* The product above.  xq int8 [M][K] and q_packed 16-byte aligned, sx [M] and
+ * d [N] fp32 4-byte aligned, y bf16 [M][N] (2-byte aligned; fp32, 4-byte
+ * aligned, for _f32), overlapping no input (W4_ERR_ARG).  0 <= M <= 262140;
+ * w4_w8_packed_bytes(N, K) < 2 GiB (else W4_ERR_SHAPE).  M == 0 or N == 0 does
+ * nothing. */
+w4_status w4_linear_w8a8(const int8_t* xq, const float* sx, int64_t M, int64_t K, const int8_t* q_packed,
+                         const float* d, int64_t N, uint16_t* y, hipStream_t stream);
+w4_status w4_linear_w8a8_f32(const int8_t* xq, const float* sx, int64_t M, int64_t K, const int8_t* q_packed,
+                             const float* d, int64_t N, float* y, hipStream_t stream);
+
+/*
+ * Rows sorted by expert: one call multiplies every row of x with the weight of
+ * its own expert, for layers of which each token uses a few experts.
+ *   offsets  [in]  int32 [experts + 1] in DEVICE memory (4-byte aligned), so
+ *                  that a router on the GPU can write them: rows offsets[e] ..
+ *                  offsets[e+1]-1 of x and y belong to expert e.  They do not
+ *                  decrease and lie in [0, M]; an expert may have no rows.
+ *                  The host does not see them, so the kernels clamp them to
+ *                  [0, M] and read a range that ends before it begins as
+ *                  empty: wrong offsets give wrong rows of y, never an access
+ *                  outside the buffers.
+ *   experts  [in]  0 <= experts <= W4_MAX_EXPERTS (0: nothing is done).
+ *   weights        of all experts, one after the other: expert e's native
+ *                  codes at q_packed + e * (its packed bytes) and its scales
+ *                  at d + e * (its scale count), every one N x K.
+ * Rows of y outside every expert's range (before offsets[0] and from
+ * offsets[experts] on) are left as they were.  A row's result does not depend
+ * on which other rows and experts the call holds.
+ */
+#define W4_MAX_EXPERTS 4096
+
+/* y = W_hat_e x with 4-bit weights, as w4_linear: the same conventions,
+ * accuracy and poisoning of non-finite rows.  x bf16 [M][K], y bf16 [M][N] (fp32
+ * for _f32), scales fp32 (bf16 bit patterns for _s16).  K at most 2^20;
+ * w4_packed_bytes(N, K) < 2 GiB; alignment and overlaps as for w4_linear. */
+w4_status w4_linear_grouped(const uint16_t* x, int64_t M, int64_t K, const int32_t* offsets, int64_t experts,
+                            const uint8_t* q_packed, const float* d_packed, int64_t N, uint16_t* y,
+                            hipStream_t stream);
+w4_status w4_linear_grouped_s16(const uint16_t* x, int64_t M, int64_t K, const int32_t* offsets, int64_t experts,
+                                const uint8_t* q_packed, const uint16_t* d_packed, int64_t N, uint16_t* y,
+                                hipStream_t stream);
+w4_status w4_linear_grouped_f32(const uint16_t* x, int64_t M, int64_t K, const int32_t* offsets, int64_t experts,
+                                const uint8_t* q_packed, const float* d_packed, int64_t N, float* y,
+                                hipStream_t stream);
+w4_status w4_linear_grouped_f32_s16(const uint16_t* x, int64_t M, int64_t K, const int32_t* offsets, int64_t experts,
+                                    const uint8_t* q_packed, const uint16_t* d_packed, int64_t N, float* y,
+                                    hipStream_t stream);
+
+/* The 8-bit product with the experts' weights (each w4_w8_packed_bytes(N, K)
+ * bytes of codes and N scales); otherwise as w4_linear_w8a8. */
+w4_status w4_linear_grouped_w8a8(const int8_t* xq, const float* sx, int64_t M, int64_t K, const int32_t* offsets,
+                                 int64_t experts, const int8_t* q_packed, const float* d, int64_t N, uint16_t* y,
+                                 hipStream_t stream);
+w4_status w4_linear_grouped_w8a8_f32(const int8_t* xq, const float* sx, int64_t M, int64_t K, const int32_t* offsets,
+                                     int64_t experts, const int8_t* q_packed, const float* d, int64_t N, float* y,
+                                     hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -31,7 +31,12 @@ What it computes (sources are the public pages this project is built from):
   error feedback (study, section 2: the GPTQ row, damping 0.01, 128-column
   blocks, no reordering; the update rule of the published GPTQ algorithm).
 
-Every function here is pinned by ``tests/test_oracle.py`` against exact
+* ``rtn_rows_ref``, ``w8a8_linear_ref`` and ``pack_w8_ref`` -- the same equation
+  with a row as the group and 8-bit codes, the int8 product with token and
+  channel scales, and the native layout of 8-bit weights.
+
+Every function here is pinned by ``tests/test_oracle.py`` (the 8-bit ones by
+``tests/test_int8_grouped.py``) against exact
 rational arithmetic, brute force on small inputs, closed forms and hand-derived
 fixtures in ``tests/golden/``; none is "parity unpinned".
 """
@@ -40,6 +45,7 @@ from .awq import (ALPHAS, awq_output_error_ref, awq_search_ref, candidate_scales
                   quantize_scaled_ref, scale_activations_ref)
 from .bf16 import bf16_bits_to_f64, f32_to_bf16_bits
 from .gptq import gptq_factor_ref, gptq_hessian_ref, gptq_quantize_ref, gptq_ref, output_error_ref
+from .int8 import QMAX8, W8A8_REL, pack_w8_ref, rtn_rows_ref, w8a8_linear_ref
 from .linear import dequantize_ref, w4_linear_ref
 from .packing import pack_canonical, unpack_canonical
 from .rtn import GROUP, NAN_BITS, QMAX, QMIN, rtn_quantize_ref
@@ -51,8 +57,10 @@ __all__ = [
     "GROUP",
     "NAN_BITS",
     "QMAX",
+    "QMAX8",
     "QMIN",
     "REL_TOL",
+    "W8A8_REL",
     "admissible",
     "awq_output_error_ref",
     "awq_search_ref",
@@ -69,9 +77,12 @@ __all__ = [
     "gptq_ref",
     "output_error_ref",
     "pack_canonical",
+    "pack_w8_ref",
     "rounding_interval",
+    "rtn_rows_ref",
     "rtn_quantize_ref",
     "unpack_canonical",
     "w4_linear_ref",
+    "w8a8_linear_ref",
     "worst_ratio",
 ]
