@@ -110,6 +110,7 @@ struct I8Args {
   const float* d;
   void* y;
   int M, K, N, experts;
+  int wide;  // every row of y starts at a multiple of 16 bytes
 };
 
 template <bool kF32>
@@ -187,6 +188,162 @@ __global__ __launch_bounds__(NW * 64) void w8a8_stream_kernel(const I8Args a) {
   }
 }
 
+// Tile form, for many rows: a block of WM x WN wavefronts owns BM = 16 WM TM rows
+// of x and BN = 16 WN TN outputs; each wavefront holds TM x TN tiles of 16 x 16
+// sums in registers.  A step is 128 inputs: the block's slices of x and of the
+// weights go to LDS straight from memory (no registers in between), one step
+// ahead of the products, in two halves of LDS.
+//
+// x is row-major, 128 bytes of a row per step: lane l of a load takes row
+// l / 8 of eight, and its 16-byte chunk (l % 8) ^ (l / 8), so that chunk c of row
+// r sits at position c ^ (r % 8) of the row's 128 bytes and the sixteen rows of
+// an operand are read without bank conflicts.
+//
+// The weights are the first operand, so a lane holds four consecutive rows of
+// the first operand, D[4 (l / 16) + e][l % 16], for one row of x.  Row 4 q + e of
+// tile j of a wavefront's four is output 16 q + 4 j + e: a lane ends with sixteen
+// consecutive outputs of its row, a wavefront with 64.  A row block's 2 KiB of a
+// step are 64 bytes apart from the next one's in LDS, which spreads the four
+// row blocks that one operand then touches over the banks.
+//
+// Rows past the tile's last and row blocks past the matrix's last re-read the
+// last one; nothing of them is stored.
+constexpr int kRowBlockLds = 2 * 1024 + 64;
+
+template <int WM, int WN, int TM, bool kF32>
+__global__ __launch_bounds__(WM* WN * 64, 1) void w8a8_tile_kernel(const I8Args a, int panels) {
+  constexpr int TN = 4;  // sixteen consecutive outputs per lane
+  constexpr int NW = WM * WN, BM = 16 * WM * TM, BN = 16 * WN * TN;
+  constexpr int kHalf = BM * 128 + BN / 16 * kRowBlockLds;  // bytes of one step
+  constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;         // 1 KiB loads per wavefront and step
+  static_assert(LA * NW * 8 == BM && LB * NW * 8 == BN, "loads shared out evenly");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kHalf];
+
+  const int tiles = count_row_tiles(a.offsets, a.experts, a.M, BM);
+  if ((int)blockIdx.x >= tiles * panels) return;
+  int t, p;
+  tile_of_block(blockIdx.x, tiles, panels, t, p);
+  RowTile rt;
+  if (!find_row_tile(a.offsets, a.experts, a.M, BM, t, rt)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nl = lane & 15, kb = lane >> 4;
+  const int wm = wave / WN, wn = wave - wm * WN;
+  const int K = a.K, nb = (a.N + kTileRows - 1) / kTileRows, rb0 = p * (BN / 16);
+  const int rows = rt.r1 - rt.r0;
+
+  const __amdgpu_buffer_rsrc_t rw =
+      make_rsrc(a.q + (int64_t)rt.expert * nb * kTileRows * K, (uint32_t)nb * kTileRows * (uint32_t)K);
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.xq + (int64_t)rt.r0 * K, (uint32_t)rows * (uint32_t)K);
+  uint32_t xo[LA], wo[LB];
+#pragma unroll
+  for (int i = 0; i < LA; ++i)
+    xo[i] = (uint32_t)min(8 * (wave * LA + i) + (lane >> 3), rows - 1) * (uint32_t)K +
+            16u * ((lane & 7) ^ (lane >> 3));
+#pragma unroll
+  for (int i = 0; i < LB; ++i) {
+    const int c = wave * LB + i;  // half c % 2 of row block c / 2
+    wo[i] = (uint32_t)min(rb0 + (c >> 1), nb - 1) * 16u * (uint32_t)K + (c & 1) * 1024u + 16u * lane;
+  }
+  typedef __attribute__((address_space(3))) void* lds_ptr;
+  auto load_step = [&](int s, int half) {
+    uint8_t* to = lds + half * kHalf;
+#pragma unroll
+    for (int i = 0; i < LA; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_ptr)(to + (wave * LA + i) * 1024), 16, (int)xo[i], s * 128, 0,
+                                               0);
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+      const int c = wave * LB + i;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rw, (lds_ptr)(to + BM * 128 + (c >> 1) * kRowBlockLds + (c & 1) * 1024), 16, (int)wo[i], s * 2048, 0, 0);
+    }
+  };
+
+  i32x4 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+
+  const uint32_t xa = (uint32_t)(wm * TM * 16 + nl) * 128u + 16u * (kb ^ (nl & 7));  // chunk kb of the lane's row
+  const uint32_t wa = (uint32_t)BM * 128u + (uint32_t)(wn * TN + (nl >> 2)) * kRowBlockLds + 256u * kb + 16u * (nl & 3);
+  i32x4 x[2][TM], w[2][TN];
+  auto read_step = [&](int half) {
+    const uint8_t* at = lds + half * kHalf;
+    // this step's slices are in LDS (every wavefront has waited for its own
+    // loads), and the other half has been read by all
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j) w[h][j] = *reinterpret_cast<const i32x4*>(at + wa + j * 64 + h * 1024);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) x[h][i] = *reinterpret_cast<const i32x4*>(at + (xa ^ (64u * h)) + i * 2048);
+    }
+  };
+  auto multiply = [&]() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = mfma16x16x64(w[h][j], x[h][i], acc[i][j]);
+  };
+  const int steps = K / 128;
+  load_step(0, 0);
+  for (int s = 0; s + 1 < steps; ++s) {
+    read_step(s & 1);
+    __builtin_amdgcn_sched_barrier(0);
+    load_step(s + 1, (s + 1) & 1);  // after the reads: they would be held up behind it
+    __builtin_amdgcn_sched_barrier(0);
+    multiply();
+  }
+  read_step((steps - 1) & 1);
+  multiply();
+
+  const int n0 = 16 * rb0 + 64 * wn + 16 * kb;  // this lane's first output
+  if (n0 >= a.N) return;
+  const int count = min(16, a.N - n0);
+  float d[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) d[e] = a.d[(int64_t)rt.expert * a.N + n0 + min(e, count - 1)];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int m = rt.r0 + 16 * (wm * TM + i) + nl;
+    if (m >= rt.r1) continue;
+    const float sx = a.sx[m];
+    float v[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = (float)acc[i][e >> 2][e & 3] * sx * d[e];
+    const int64_t at = (int64_t)m * a.N + n0;
+    if constexpr (kF32) {
+      float* y = static_cast<float*>(a.y) + at;
+      if (a.wide && count == 16) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(y + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (e < count) y[e] = v[e];
+      }
+    } else {
+      uint16_t* y = static_cast<uint16_t*>(a.y) + at;
+      if (a.wide && count == 16) {
+        uint32_t u[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          u[e] = (uint32_t)f32_to_bf16_rne(v[2 * e]) | (uint32_t)f32_to_bf16_rne(v[2 * e + 1]) << 16;
+        *reinterpret_cast<uint4*>(y) = make_uint4(u[0], u[1], u[2], u[3]);
+        *reinterpret_cast<uint4*>(y + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (e < count) y[e] = f32_to_bf16_rne(v[e]);
+      }
+    }
+  }
+}
+
 }  // namespace
 
 hipError_t launch_quantize_w8(const float* W, int64_t N, int64_t K, int8_t* q, float* d, hipStream_t stream) {
@@ -218,8 +375,18 @@ hipError_t launch_pack_w8(const int8_t* src, int64_t N, int64_t K, int8_t* dst, 
 hipError_t launch_linear_w8a8(const int8_t* xq, const float* sx, int64_t M, int64_t K, const int32_t* offsets,
                               int64_t experts, const int8_t* q, const float* d, int64_t N, void* y, bool f32,
                               hipStream_t stream) {
-  const I8Args a{xq, sx, offsets, q, d, y, (int)M, (int)K, (int)N, (int)experts};
+  const I8Args a{xq, sx, offsets, q, d, y, (int)M, (int)K, (int)N, (int)experts,
+                 (reinterpret_cast<uintptr_t>(y) | (uintptr_t)(N * (f32 ? 4 : 2))) % 16 == 0};
   const int64_t nb = (N + kTileRows - 1) / kTileRows;
+  if (M > 64 * experts) {
+    const int64_t tiles = max_row_tiles(M, experts, offsets != nullptr, 256), panels = (nb + 15) / 16;
+    if (tiles * panels > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+    if (f32)
+      w8a8_tile_kernel<2, 4, 8, true><<<(unsigned)(tiles * panels), 512, 0, stream>>>(a, (int)panels);
+    else
+      w8a8_tile_kernel<2, 4, 8, false><<<(unsigned)(tiles * panels), 512, 0, stream>>>(a, (int)panels);
+    return hipGetLastError();
+  }
   const int64_t blocks = max_row_tiles(M, experts, offsets != nullptr, 16) * nb;
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   if (f32)

@@ -57,6 +57,34 @@ __device__ __forceinline__ bool find_row_tile(const int* __restrict__ offsets, i
   return false;
 }
 
+// Row tiles there are in all.  Every lane of the wavefront must call this.
+__device__ __forceinline__ int count_row_tiles(const int* __restrict__ offsets, int experts, int M, int BM) {
+  if (!offsets) return (M + BM - 1) / BM;
+  int n = 0;
+  for (int e = threadIdx.x & 63; e < experts; e += 64) {
+    const int a = min(max(offsets[e], 0), M), b = min(max(offsets[e + 1], 0), M);
+    n += b > a ? (b - a + BM - 1) / BM : 0;
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) n += __shfl_xor(n, d);
+  return __builtin_amdgcn_readfirstlane(n);
+}
+
+// Which (row tile, panel of outputs) block b of tiles * panels runs.  Blocks go to
+// the eight XCDs in turn, each with an L2 of its own, so each XCD is given a
+// contiguous run of the work: bands of kBand row tiles, panel by panel within a
+// band, so that the blocks that run at one time on an XCD share their rows and
+// their panels.
+constexpr int kXcds = 8, kBand = 4;
+__device__ __forceinline__ void tile_of_block(int b, int tiles, int panels, int& t, int& p) {
+  const int total = tiles * panels, xcd = b % kXcds;
+  const int at = xcd * (total / kXcds) + min(xcd, total % kXcds) + b / kXcds;
+  const int band = at / (kBand * panels), in = at - band * kBand * panels;
+  const int height = min(kBand, tiles - band * kBand);
+  p = in / height;
+  t = band * kBand + in - p * height;
+}
+
 // Row tiles a launch has to cover (see above).
 inline int64_t max_row_tiles(int64_t M, int64_t experts, bool grouped, int BM) {
   if (!grouped) return (M + BM - 1) / BM;
