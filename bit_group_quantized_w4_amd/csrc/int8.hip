@@ -18,6 +18,7 @@
 
 #include <float.h>
 
+
 namespace w4 {
 namespace {
 
@@ -123,185 +124,9 @@ __device__ __forceinline__ void store_scaled(const I8Args& a, int m, int n, int 
     static_cast<uint16_t*>(a.y)[i] = f32_to_bf16_rne(v);
 }
 
-// Streaming form: a block owns R row blocks of 16 outputs and one tile of 16 MT
-// rows of x; its NW wavefronts divide K.  Lane l of a wavefront holds
-// A[l % 16][16 (l / 16) .. + 15] of x, the tile's B operand and
-// D[4 (l / 16) + j][l % 16], j = 0..3.
-template <int MT, int R, int NW, bool kF32>
-__global__ __launch_bounds__(NW * 64) void w8a8_stream_kernel(const I8Args a) {
-  const int nb = (a.N + kTileRows - 1) / kTileRows, panels = (nb + R - 1) / R;
-  const int t = blockIdx.x / panels, rb0 = (blockIdx.x - t * panels) * R;
-  RowTile rt;
-  if (!find_row_tile(a.offsets, a.experts, a.M, 16 * MT, t, rt)) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nl = lane & 15, kb = lane >> 4;
-  const int steps = a.K / kStep;
-  const int s0 = (int)((int64_t)steps * wave / NW), s1 = (int)((int64_t)steps * (wave + 1) / NW);
-
-  const __amdgpu_buffer_rsrc_t rw =
-      make_rsrc(a.q + (int64_t)rt.expert * nb * kTileRows * a.K, (uint32_t)nb * kTileRows * (uint32_t)a.K);
-  const __amdgpu_buffer_rsrc_t rx =
-      make_rsrc(a.xq + (int64_t)rt.r0 * a.K, (uint32_t)(rt.r1 - rt.r0) * (uint32_t)a.K);
-  uint32_t wo[R], xo[MT];
-#pragma unroll
-  for (int r = 0; r < R; ++r) wo[r] = rb0 + r < nb ? ((uint32_t)(rb0 + r) * steps * 64u + lane) * 16u : kOob;
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-    xo[i] = 16 * i + nl < rt.r1 - rt.r0 ? (uint32_t)(16 * i + nl) * (uint32_t)a.K + 16u * kb : kOob;
-
-  i32x4 acc[MT][R];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int r = 0; r < R; ++r) acc[i][r] = i32x4{0, 0, 0, 0};
-  for (int s = s0; s < s1; ++s) {
-    i32x4 w[R], x[MT];
-#pragma unroll
-    for (int r = 0; r < R; ++r) w[r] = bitcast<i32x4>(bload<0>(rw, wo[r] + (uint32_t)s * 1024u));
-#pragma unroll
-    for (int i = 0; i < MT; ++i) x[i] = bitcast<i32x4>(bload<0>(rx, xo[i] + (uint32_t)s * kStep));
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int r = 0; r < R; ++r) acc[i][r] = mfma16x16x64(x[i], w[r], acc[i][r]);
-  }
-
-  __shared__ i32x4 red[NW][MT * R][64];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int r = 0; r < R; ++r) red[wave][i * R + r][lane] = acc[i][r];
-  __syncthreads();
-  for (int c = wave; c < MT * R; c += NW) {
-    const int i = c / R, r = c - i * R;
-    const int n = (rb0 + r) * kTileRows + nl;
-    if (n >= a.N) continue;
-    i32x4 v = red[0][c][lane];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) v += red[w][c][lane];
-    const float d = a.d[(int64_t)rt.expert * a.N + n];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = rt.r0 + 16 * i + 4 * kb + j;
-      if (m < rt.r1) store_scaled<kF32>(a, m, n, v[j], a.sx[m], d);
-    }
-  }
-}
-
-// Tile form, for many rows: a block of WM x WN wavefronts owns BM = 16 WM TM rows
-// of x and BN = 16 WN TN outputs; each wavefront holds TM x TN tiles of 16 x 16
-// sums in registers.  A step is 128 inputs: the block's slices of x and of the
-// weights go to LDS straight from memory (no registers in between), one step
-// ahead of the products, in two halves of LDS.
-//
-// x is row-major, 128 bytes of a row per step: lane l of a load takes row
-// l / 8 of eight, and its 16-byte chunk (l % 8) ^ (l / 8), so that chunk c of row
-// r sits at position c ^ (r % 8) of the row's 128 bytes and the sixteen rows of
-// an operand are read without bank conflicts.
-//
-// The weights are the first operand, so a lane holds four consecutive rows of
-// the first operand, D[4 (l / 16) + e][l % 16], for one row of x.  Row 4 q + e of
-// tile j of a wavefront's four is output 16 q + 4 j + e: a lane ends with sixteen
-// consecutive outputs of its row, a wavefront with 64.  A row block's 2 KiB of a
-// step are 64 bytes apart from the next one's in LDS, which spreads the four
-// row blocks that one operand then touches over the banks.
-//
-// Rows past the tile's last and row blocks past the matrix's last re-read the
-// last one; nothing of them is stored.
-constexpr int kRowBlockLds = 2 * 1024 + 64;
-
-template <int WM, int WN, int TM, bool kF32>
-__global__ __launch_bounds__(WM* WN * 64, 1) void w8a8_tile_kernel(const I8Args a, int panels) {
-  constexpr int TN = 4;  // sixteen consecutive outputs per lane
-  constexpr int NW = WM * WN, BM = 16 * WM * TM, BN = 16 * WN * TN;
-  constexpr int kHalf = BM * 128 + BN / 16 * kRowBlockLds;  // bytes of one step
-  constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;         // 1 KiB loads per wavefront and step
-  static_assert(LA * NW * 8 == BM && LB * NW * 8 == BN, "loads shared out evenly");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kHalf];
-
-  const int tiles = count_row_tiles(a.offsets, a.experts, a.M, BM);
-  if ((int)blockIdx.x >= tiles * panels) return;
-  int t, p;
-  tile_of_block(blockIdx.x, tiles, panels, t, p);
-  RowTile rt;
-  if (!find_row_tile(a.offsets, a.experts, a.M, BM, t, rt)) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nl = lane & 15, kb = lane >> 4;
-  const int wm = wave / WN, wn = wave - wm * WN;
-  const int K = a.K, nb = (a.N + kTileRows - 1) / kTileRows, rb0 = p * (BN / 16);
-  const int rows = rt.r1 - rt.r0;
-
-  const __amdgpu_buffer_rsrc_t rw =
-      make_rsrc(a.q + (int64_t)rt.expert * nb * kTileRows * K, (uint32_t)nb * kTileRows * (uint32_t)K);
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.xq + (int64_t)rt.r0 * K, (uint32_t)rows * (uint32_t)K);
-  uint32_t xo[LA], wo[LB];
-#pragma unroll
-  for (int i = 0; i < LA; ++i)
-    xo[i] = (uint32_t)min(8 * (wave * LA + i) + (lane >> 3), rows - 1) * (uint32_t)K +
-            16u * ((lane & 7) ^ (lane >> 3));
-#pragma unroll
-  for (int i = 0; i < LB; ++i) {
-    const int c = wave * LB + i;  // half c % 2 of row block c / 2
-    wo[i] = (uint32_t)min(rb0 + (c >> 1), nb - 1) * 16u * (uint32_t)K + (c & 1) * 1024u + 16u * lane;
-  }
-  typedef __attribute__((address_space(3))) void* lds_ptr;
-  auto load_step = [&](int s, int half) {
-    uint8_t* to = lds + half * kHalf;
-#pragma unroll
-    for (int i = 0; i < LA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_ptr)(to + (wave * LA + i) * 1024), 16, (int)xo[i], s * 128, 0,
-                                               0);
-#pragma unroll
-    for (int i = 0; i < LB; ++i) {
-      const int c = wave * LB + i;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rw, (lds_ptr)(to + BM * 128 + (c >> 1) * kRowBlockLds + (c & 1) * 1024), 16, (int)wo[i], s * 2048, 0, 0);
-    }
-  };
-
-  i32x4 acc[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-
-  const uint32_t xa = (uint32_t)(wm * TM * 16 + nl) * 128u + 16u * (kb ^ (nl & 7));  // chunk kb of the lane's row
-  const uint32_t wa = (uint32_t)BM * 128u + (uint32_t)(wn * TN + (nl >> 2)) * kRowBlockLds + 256u * kb + 16u * (nl & 3);
-  i32x4 x[2][TM], w[2][TN];
-  auto read_step = [&](int half) {
-    const uint8_t* at = lds + half * kHalf;
-    // this step's slices are in LDS (every wavefront has waited for its own
-    // loads), and the other half has been read by all
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int j = 0; j < TN; ++j) w[h][j] = *reinterpret_cast<const i32x4*>(at + wa + j * 64 + h * 1024);
-#pragma unroll
-      for (int i = 0; i < TM; ++i) x[h][i] = *reinterpret_cast<const i32x4*>(at + (xa ^ (64u * h)) + i * 2048);
-    }
-  };
-  auto multiply = [&]() {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = mfma16x16x64(w[h][j], x[h][i], acc[i][j]);
-  };
-  const int steps = K / 128;
-  load_step(0, 0);
-  for (int s = 0; s + 1 < steps; ++s) {
-    read_step(s & 1);
-    __builtin_amdgcn_sched_barrier(0);
-    load_step(s + 1, (s + 1) & 1);  // after the reads: they would be held up behind it
-    __builtin_amdgcn_sched_barrier(0);
-    multiply();
-  }
-  read_step((steps - 1) & 1);
-  multiply();
-
-  const int n0 = 16 * rb0 + 64 * wn + 16 * kb;  // this lane's first output
+// Sums of TM row tiles, sixteen consecutive outputs from n0 on of rows m0, m0 + 16 ..., scaled and stored.
+template <int TM, bool kF32>
+__device__ __forceinline__ void store_tile(const I8Args& a, const RowTile& rt, int m0, int n0, const i32x4 (&acc)[TM][4]) {
   if (n0 >= a.N) return;
   const int count = min(16, a.N - n0);
   float d[16];
@@ -309,7 +134,7 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void w8a8_tile_kernel(const I8Args 
   for (int e = 0; e < 16; ++e) d[e] = a.d[(int64_t)rt.expert * a.N + n0 + min(e, count - 1)];
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int m = rt.r0 + 16 * (wm * TM + i) + nl;
+    const int m = m0 + 16 * i;
     if (m >= rt.r1) continue;
     const float sx = a.sx[m];
     float v[16];
@@ -342,6 +167,497 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void w8a8_tile_kernel(const I8Args 
       }
     }
   }
+}
+
+// Streaming form, for few rows: a block owns R row blocks of 16 outputs and one
+// tile of 16 MT rows of x; its NW wavefronts divide K.  Lane l of a wavefront holds
+// A[l % 16][16 (l / 16) .. + 15] of x, the tile's B operand and
+// D[4 (l / 16) + j][l % 16], j = 0..3, all straight from memory.
+//
+// Bound by the weight stream: 13 rows of 28672 x 8192 take 41.5 us (5.7 TB/s).
+// kStream reads the weights past the caches (47.6 us without).  Weights that may
+// still lie in the 256 MB last-level cache from their last use are read through
+// it: 2560 x 9216 at one row takes 6.6 us against 9.3 us.
+template <int MT, int R, int NW, bool kStream, bool kF32>
+__global__ __launch_bounds__(NW * 64) void w8a8_stream_kernel(const I8Args a) {
+  constexpr int kWide = MT > R ? MT : R;
+  constexpr int D = kWide >= 4 ? 2 : 8 / kWide;  // steps in flight: about 8 KiB per wavefront
+  const int nb = (a.N + kTileRows - 1) / kTileRows, panels = (nb + R - 1) / R;
+  const int t = blockIdx.x / panels, rb0 = (blockIdx.x - t * panels) * R;
+  RowTile rt;
+  if (!find_row_tile(a.offsets, a.experts, a.M, 16 * MT, t, rt)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nl = lane & 15, kb = lane >> 4;
+  const int steps = a.K / kStep;
+  const int s0 = (int)((int64_t)steps * wave / NW), s1 = (int)((int64_t)steps * (wave + 1) / NW);
+
+  const __amdgpu_buffer_rsrc_t rw =
+      make_rsrc(a.q + (int64_t)rt.expert * nb * kTileRows * a.K, (uint32_t)nb * kTileRows * (uint32_t)a.K);
+  const __amdgpu_buffer_rsrc_t rx =
+      make_rsrc(a.xq + (int64_t)rt.r0 * a.K, (uint32_t)(rt.r1 - rt.r0) * (uint32_t)a.K);
+  uint32_t wo[R], xo[MT];
+#pragma unroll
+  for (int r = 0; r < R; ++r) wo[r] = rb0 + r < nb ? ((uint32_t)(rb0 + r) * steps * 64u + lane) * 16u : kOob;
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+    xo[i] = 16 * i + nl < rt.r1 - rt.r0 ? (uint32_t)(16 * i + nl) * (uint32_t)a.K + 16u * kb : kOob;
+
+  i32x4 acc[MT][R];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[i][r] = i32x4{0, 0, 0, 0};
+  // a ring of D steps' operands; a step past the wavefront's last reads zeros
+  // without touching memory, so that every load is unconditional
+  uint4 w[D][R], x[D][MT];
+  auto issue = [&](int c, int s) {
+    const uint32_t ow = s < s1 ? (uint32_t)s * 1024u : kOob, ox = s < s1 ? (uint32_t)s * kStep : kOob;
+#pragma unroll
+    for (int r = 0; r < R; ++r) w[c][r] = bload<kStream ? kNonTemporal : 0>(rw, wo[r] + ow);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) x[c][i] = bload<0>(rx, xo[i] + ox);
+  };
+#pragma unroll
+  for (int c = 0; c < D; ++c) {
+    issue(c, s0 + c);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  for (int s = s0; s < s1; s += D) {
+#pragma unroll
+    for (int c = 0; c < D; ++c) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[i][r] = mfma16x16x64(bitcast<i32x4>(x[c][i]), bitcast<i32x4>(w[c][r]), acc[i][r]);
+      issue(c, s + c + D);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+
+  __shared__ i32x4 red[NW][MT * R][64];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int r = 0; r < R; ++r) red[wave][i * R + r][lane] = acc[i][r];
+  __syncthreads();
+  for (int c = wave; c < MT * R; c += NW) {
+    const int i = c / R, r = c - i * R;
+    const int n = (rb0 + r) * kTileRows + nl;
+    if (n >= a.N) continue;
+    i32x4 v = red[0][c][lane];
+#pragma unroll
+    for (int w_ = 1; w_ < NW; ++w_) v += red[w_][c][lane];
+    const float d = a.d[(int64_t)rt.expert * a.N + n];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int m = rt.r0 + 16 * i + 4 * kb + j;
+      if (m < rt.r1) store_scaled<kF32>(a, m, n, v[j], a.sx[m], d);
+    }
+  }
+}
+
+// Tile form, for many rows: a block of WM x WN wavefronts owns BM = 16 WM TM rows
+// of x and BN = 64 WN outputs; each wavefront holds TM x 4 tiles of 16 x 16 sums
+// in registers.  A step is 128 inputs: the block's slices of x and of the weights
+// go to LDS straight from memory (no registers in between), one step ahead of the
+// products, in two LDS buffers.
+//
+// x is row-major, 128 bytes of a row per step: lane l of a load takes row
+// l / 8 of eight, and its 16-byte chunk (l % 8) ^ (l / 8), so that chunk c of row
+// r sits at position c ^ (r % 8) of the row's 128 bytes and the sixteen rows of
+// an operand are read without bank conflicts.  (Steps of 64 inputs in four
+// buffers, three steps ahead, took half lines of x: 7% slower at 256 x 256.)
+//
+// The weights are the first operand, so a lane holds four consecutive rows of
+// the first operand, D[4 (l / 16) + e][l % 16], for one row of x.  Row 4 q + e of
+// tile j of a wavefront's four is output 16 q + 4 j + e: a lane ends with sixteen
+// consecutive outputs of its row, a wavefront with 64.  A row block's 2 KiB of a
+// step are 64 bytes apart from the next one's in LDS, which spreads the four
+// row blocks that one operand then touches over the banks.
+//
+// The products of a step run in four parts (half of the rows times half of the
+// inputs).  Operands are read from LDS one part ahead, beside the products of the
+// part before, and the next step's loads are issued beside the first part: one
+// load holds up the wavefront for the 16 cycles that the address unit of the CU
+// takes for it, which eight wavefronts would otherwise spend in turn before any
+// product (4096 rows of 17408 x 5120: 361 us with all reads and loads first, 338
+// with both spread; 2161 TOP/s).  At that rate the power limit lowers the clock.
+//
+// Rows past the tile's last, row blocks past the matrix's last and steps past the
+// last one lie outside their buffers: such loads read no memory and give zeros.
+constexpr int kRowBlockLds = 2 * 1024 + 64;
+
+template <int WM, int WN, int TM, int OCC, bool kF32>
+__global__ __launch_bounds__(WM* WN * 64, OCC) void w8a8_tile_kernel(const I8Args a, int panels) {
+  constexpr int TN = 4;       // sixteen consecutive outputs per lane
+  constexpr int TH = TM / 2;  // row tiles per part
+  constexpr int NW = WM * WN, BM = 16 * WM * TM, BN = 16 * WN * TN;
+  constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // 1 KiB loads per wavefront and step
+  static_assert(LA * NW * 8 == BM && LB * NW * 8 == BN && LB % 2 == 0 && TH * 2 == TM, "loads shared out evenly");
+  constexpr int kX = BM * 128, kBuffer = kX + BN / 16 * kRowBlockLds;
+  // two variables, each named outright where it is used: the compiler then knows
+  // that loads into one are no reason to wait before reading the other
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[kBuffer], lds1[kBuffer];
+
+  // (offsets whose ranges overlap could make more tiles than the launch covers)
+  const int tiles = min(count_row_tiles(a.offsets, a.experts, a.M, BM), (int)gridDim.x / panels);
+  if ((int)blockIdx.x >= tiles * panels) return;
+  int t, p;
+  tile_of_block(blockIdx.x, tiles, panels, t, p);
+  RowTile rt;
+  if (!find_row_tile(a.offsets, a.experts, a.M, BM, t, rt)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nl = lane & 15, kb = lane >> 4;
+  const int wm = wave / WN, wn = wave - wm * WN;
+  const int K = a.K, nb = (a.N + kTileRows - 1) / kTileRows, rb0 = p * (BN / 16);
+  const int rows = rt.r1 - rt.r0, steps = K / 128;
+
+  const __amdgpu_buffer_rsrc_t rw =
+      make_rsrc(a.q + (int64_t)rt.expert * nb * kTileRows * K, (uint32_t)nb * kTileRows * (uint32_t)K);
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.xq + (int64_t)rt.r0 * K, (uint32_t)rows * (uint32_t)K);
+  const uint32_t xo = (uint32_t)(8 * wave * LA + (lane >> 3)) * (uint32_t)K + 16u * ((lane & 7) ^ (lane >> 3));
+  const uint32_t wo = (uint32_t)(rb0 + wave * LB / 2) * 16u * (uint32_t)K + 16u * lane;
+  typedef __attribute__((address_space(3))) void* lds_ptr;
+  // load i of this wavefront's for step s (zeros past the last step)
+  auto load = [&](int i, int s, uint8_t* to) {
+    if (i < LA) {
+      const uint32_t k = s < steps ? (uint32_t)s * 128u : kOob;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_ptr)(to + (wave * LA + i) * 1024), 16,
+                                               (int)(xo + (uint32_t)(8 * i * K) + k), 0, 0, 0);
+    } else {
+      const uint32_t k = s < steps ? (uint32_t)s * 2048u : kOob;
+      const int r = (i - LA) >> 1, h = (i - LA) & 1;  // row block, half of the step
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_ptr)(to + kX + (wave * LB / 2 + r) * kRowBlockLds + h * 1024), 16,
+                                               (int)(wo + (uint32_t)(16 * r * K + 1024 * h) + k), 0, 0, 0);
+    }
+  };
+  auto load_step = [&](int s, uint8_t* to) {
+#pragma unroll
+    for (int i = 0; i < LA + LB; ++i) load(i, s, to);
+  };
+  // Every load into LDS and every read of it that this wavefront has issued is
+  // done, and so are the other wavefronts'.
+  auto all_done = [] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  i32x4 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+
+  const uint32_t xa = (uint32_t)(wm * TM * 16 + nl) * 128u + 16u * (kb ^ (nl & 7));
+  const uint32_t wa = (uint32_t)kX + (uint32_t)(wn * TN + (nl >> 2)) * kRowBlockLds + 256u * kb + 16u * (nl & 3);
+  i32x4 x[2][TH], w[2][TN];  // x by row half, w by input half
+  auto read_w = [&](int h, int j, const uint8_t* from) {
+    w[h][j] = *reinterpret_cast<const i32x4*>(from + wa + j * 64 + h * 1024);
+  };
+  auto read_x = [&](int h, int c, int i, const uint8_t* from) {
+    x[c][i] = *reinterpret_cast<const i32x4*>(from + (xa ^ (64u * h)) + (c * TH + i) * 2048);
+  };
+  // the products of row half c and input half h; beside(i) comes before row tile i's
+  auto multiply = [&](int c, int h, auto beside) {
+#pragma unroll
+    for (int i = 0; i < TH; ++i) {
+      beside(i);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[c * TH + i][j] = mfma16x16x64(w[h][j], x[c][i], acc[c * TH + i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto operands_ready = [] {
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // A step whose slices are in `cur`, with the last part of the step before; its
+  // own last part is left to the next.
+  auto step = [&](int s, uint8_t* cur, uint8_t* nxt) {
+    constexpr int kLoads = LA + LB, kReads = TN + TH;
+    auto read = [&](int h, int i) {  // share i of TH of input half h's operands
+#pragma unroll
+      for (int r = (i * kReads + TH - 1) / TH; r < ((i + 1) * kReads + TH - 1) / TH; ++r) {
+        if (r < TN) read_w(h, r, cur);
+        else read_x(h, 0, r - TN, cur);
+      }
+    };
+    all_done();  // `cur` is filled, and nothing reads `nxt` any more
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(1, 1, [&](int i) {
+#pragma unroll
+      for (int l = i * kLoads / TH; l < (i + 1) * kLoads / TH; ++l) load(l, s + 1, nxt);
+      read(0, i);
+    });
+    operands_ready();
+    multiply(0, 0, [&](int i) { read_x(0, 1, i, cur); });
+    operands_ready();
+    multiply(1, 0, [&](int i) { read(1, i); });
+    operands_ready();
+    multiply(0, 1, [&](int i) { read_x(1, 1, i, cur); });
+  };
+
+  load_step(0, lds0);
+#pragma unroll
+  for (int j = 0; j < TN; ++j) w[1][j] = i32x4{0, 0, 0, 0};  // no step before the first
+#pragma unroll
+  for (int i = 0; i < TH; ++i) x[1][i] = i32x4{0, 0, 0, 0};
+  for (int s = 0; s < steps; s += 2) {  // an odd last step is followed by one of zeros
+    step(s, lds0, lds1);
+    step(s + 1, lds1, lds0);
+  }
+  multiply(1, 1, [](int) {});
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load into LDS outlives the block
+
+  store_tile<TM, kF32>(a, rt, rt.r0 + 16 * wm * TM + nl, 16 * rb0 + 64 * wn + 16 * kb, acc);
+}
+
+// The same for fewer rows, where a launch has too few tiles to fill the GPU and
+// each block's time is the latency of its loads: smaller tiles, steps of 64 inputs
+// in four LDS buffers, loaded three steps ahead, and G groups of WM x WN
+// wavefronts that divide K and add their sums at the end.
+//
+// 64 bytes of a row per step: lane l of a load takes row l / 4 of sixteen and its
+// chunk (l % 4) ^ t, t = 0, 2, 3, 1 for rows 0-3, 4-7, 8-11, 12-15, which keeps the
+// operand reads free of bank conflicts (LDS serves lanes 0-3, 12-15 and 20-27 of
+// a 16-byte read together).  333 rows of 2561 x 9216: 25.8 us with 64 x 64 tiles and
+// two groups, 52.2 us as 128 x 128 tiles of the kernel above, 30.6 us streamed.
+__device__ __forceinline__ uint32_t quad_swizzle(int t) { return (0x78u >> (2 * t)) & 3u; }
+
+template <int WM, int WN, int TM, int G, bool kF32>
+__global__ __launch_bounds__(WM* WN* G * 64) void w8a8_deep_kernel(const I8Args a, int panels) {
+  constexpr int TN = 4, TH = TM / 2;
+  constexpr int NW = WM * WN, BM = 16 * WM * TM, BN = 16 * WN * TN;
+  constexpr int LA = BM / 16 / NW, LB = BN / 16 / NW;  // 1 KiB loads per wavefront and step
+  static_assert(LA * NW * 16 == BM && LB * NW * 16 == BN && TH * 2 == TM, "loads shared out evenly");
+  constexpr int kRowBlock = 1024 + 64;
+  constexpr int kX = BM * 64, kBuffer = kX + BN / 16 * kRowBlock;
+  static_assert(TM * TN * NW * 1024 <= 4 * kBuffer, "a group's sums fit its buffers");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[G * kBuffer], lds1[G * kBuffer], lds2[G * kBuffer],
+      lds3[G * kBuffer];
+
+  // (offsets whose ranges overlap could make more tiles than the launch covers)
+  const int tiles = min(count_row_tiles(a.offsets, a.experts, a.M, BM), (int)gridDim.x / panels);
+  if ((int)blockIdx.x >= tiles * panels) return;
+  int t, p;
+  tile_of_block(blockIdx.x, tiles, panels, t, p);
+  RowTile rt;
+  if (!find_row_tile(a.offsets, a.experts, a.M, BM, t, rt)) return;
+  const int lane = threadIdx.x & 63, wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nl = lane & 15, kb = lane >> 4;
+  const int g = wave_all / NW, wave = wave_all - g * NW;
+  const int wm = wave / WN, wn = wave - wm * WN;
+  const int K = a.K, nb = (a.N + kTileRows - 1) / kTileRows, rb0 = p * (BN / 16);
+  const int rows = rt.r1 - rt.r0, steps = K / kStep;
+  const int per = (steps + G - 1) / G, first = g * per, last = min(first + per, steps);  // the group's steps
+
+  const __amdgpu_buffer_rsrc_t rw =
+      make_rsrc(a.q + (int64_t)rt.expert * nb * kTileRows * K, (uint32_t)nb * kTileRows * (uint32_t)K);
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.xq + (int64_t)rt.r0 * K, (uint32_t)rows * (uint32_t)K);
+  const uint32_t xo = (uint32_t)(16 * wave * LA + (lane >> 2)) * (uint32_t)K + 16u * ((lane & 3) ^ quad_swizzle(lane >> 4));
+  const uint32_t wo = (uint32_t)(rb0 + wave * LB) * 16u * (uint32_t)K + 16u * lane;
+  typedef __attribute__((address_space(3))) void* lds_ptr;
+  auto load = [&](int i, int s, uint8_t* to) {
+    to += g * kBuffer;
+    if (i < LA) {
+      const uint32_t k = s < last ? (uint32_t)s * 64u : kOob;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_ptr)(to + (wave * LA + i) * 1024), 16,
+                                               (int)(xo + (uint32_t)(16 * i * K) + k), 0, 0, 0);
+    } else {
+      const uint32_t k = s < last ? (uint32_t)s * 1024u : kOob;
+      const int r = i - LA;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_ptr)(to + kX + (wave * LB + r) * kRowBlock), 16,
+                                               (int)(wo + (uint32_t)(16 * r * K) + k), 0, 0, 0);
+    }
+  };
+  auto load_step = [&](int s, uint8_t* to) {
+#pragma unroll
+    for (int i = 0; i < LA + LB; ++i) load(i, s, to);
+  };
+
+  i32x4 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  const uint32_t xa = (uint32_t)(g * kBuffer) + (uint32_t)(wm * TM * 16 + nl) * 64u + 16u * (kb ^ quad_swizzle(nl >> 2));
+  const uint32_t wa = (uint32_t)(g * kBuffer + kX) + (uint32_t)(wn * TN + (nl >> 2)) * kRowBlock + 256u * kb + 16u * (nl & 3);
+  i32x4 x[2][TH], w[2][TN];  // x by row half, w by step parity
+  auto multiply = [&](int c, int v, auto beside) {
+#pragma unroll
+    for (int i = 0; i < TH; ++i) {
+      beside(i);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[c * TH + i][j] = mfma16x16x64(w[v][j], x[c][i], acc[c * TH + i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto step = [&](int s, int v, uint8_t* cur, uint8_t* prev) {
+    constexpr int kLoads = LA + LB, kReads = TN + TH;
+    asm volatile("" ::: "memory");
+    constexpr int kLeft = 2 * kLoads;  // vmcnt: the last two steps' loads; lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt(0x0070 | (kLeft & 15) | (kLeft >> 4) << 14);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(1, v ^ 1, [&](int i) {  // the last part of the step before
+#pragma unroll
+      for (int l = i * kLoads / TH; l < (i + 1) * kLoads / TH; ++l) load(l, s + 3, prev);
+#pragma unroll
+      for (int r = (i * kReads + TH - 1) / TH; r < ((i + 1) * kReads + TH - 1) / TH; ++r) {
+        if (r < TN) w[v][r] = *reinterpret_cast<const i32x4*>(cur + wa + r * 64);
+        else x[0][r - TN] = *reinterpret_cast<const i32x4*>(cur + xa + (r - TN) * 1024);
+      }
+    });
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(0, v, [&](int i) { x[1][i] = *reinterpret_cast<const i32x4*>(cur + xa + (TH + i) * 1024); });
+  };
+#pragma unroll
+  for (int j = 0; j < TN; ++j) w[1][j] = i32x4{0, 0, 0, 0};  // no step before the first
+#pragma unroll
+  for (int i = 0; i < TH; ++i) x[1][i] = i32x4{0, 0, 0, 0};
+  load_step(first, lds0);
+  load_step(first + 1, lds1);
+  load_step(first + 2, lds2);
+  for (int s = 0; s < per; s += 4) {  // every group takes the same number of steps, zeros at the end
+    step(first + s, 0, lds0, lds3);
+    step(first + s + 1, 1, lds1, lds0);
+    step(first + s + 2, 0, lds2, lds1);
+    step(first + s + 3, 1, lds3, lds2);
+  }
+  multiply(1, 1, [](int) {});
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0): no load into LDS outlives the loop
+  if constexpr (G > 1) {
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    // chunk c of a group's sums, 1 KiB per wavefront, in buffer c % 4
+    auto chunk = [&](int gg, int c) {
+      uint8_t* b = c % 4 == 0 ? lds0 : c % 4 == 1 ? lds1 : c % 4 == 2 ? lds2 : lds3;
+      return reinterpret_cast<i32x4*>(b + gg * kBuffer + ((c / 4) * NW + wave) * 1024 + 16 * lane);
+    };
+    if (g > 0) {
+#pragma unroll
+      for (int c = 0; c < TM * TN; ++c) *chunk(g, c) = acc[c / TN][c % TN];
+    }
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int gg = 1; gg < G; ++gg)
+#pragma unroll
+      for (int c = 0; c < TM * TN; ++c) acc[c / TN][c % TN] += *chunk(gg, c);
+  }
+  store_tile<TM, kF32>(a, rt, rt.r0 + 16 * wm * TM + nl, 16 * rb0 + 64 * wn + 16 * kb, acc);
+}
+
+// ---------------------------------------------------------------------------
+// launch configuration
+// ---------------------------------------------------------------------------
+enum class W8a8 { kTile256, kTile128, kDeep128, kDeep64x128, kDeep64, kStream32x64, kStream16x64, kRows16 };
+
+// The kernel for M rows shared out over `experts` matrices of N x K (their true
+// sizes are on the GPU: all are taken to be as busy as the average one).  Up to 16
+// rows each the weight stream is all there is to do.  Beyond that the smallest
+// estimate wins, in us per 128 inputs, from times measured on the 2560 x 9216,
+// 9216 x 2560, 28672 x 8192 and 17408 x 5120 matrices at 32 to 4096 rows: `one` while
+// every block has a CU for itself, `all` for each further full set of `slots` blocks.
+// Small tiles win until the larger ones fill the GPU: 512 rows of 2560 x 9216 take
+// 27 us as 64 x 128 (160 blocks), 35 us as 64 x 64 and 48 us as 128 x 128 (80 blocks);
+// at 2048 rows 69, 82 and 60 us.
+W8a8 choose_w8a8(int64_t M, int64_t N, int64_t K, int64_t experts) {
+  const int64_t busy = experts < M ? experts : M, rows = (M + busy - 1) / busy;
+  if (rows <= 16) return W8a8::kRows16;
+  struct Shape {
+    W8a8 kind;
+    int BM, BN, slots;
+    double one, all;
+  };
+  static const Shape shapes[] = {
+      {W8a8::kTile256, 256, 256, 256, 1.68, 1.68},     {W8a8::kTile128, 128, 128, 512, 0.66, 1.07},
+      {W8a8::kDeep128, 128, 128, 512, 0.52, 1.24},     {W8a8::kDeep64x128, 64, 128, 768, 0.40, 1.40},
+      {W8a8::kDeep64, 64, 64, 512, 0.34, 0.70},        {W8a8::kStream32x64, 32, 64, 256, 0.22, 0.33},
+      {W8a8::kStream16x64, 16, 64, 256, 0.17, 0.21},
+  };
+  W8a8 best = W8a8::kTile256;
+  double least = 0;
+  for (const Shape& s : shapes) {
+    const int64_t blocks = busy * ((rows + s.BM - 1) / s.BM) * ((N + s.BN - 1) / s.BN);
+    double cost = s.one;
+    if (blocks > 256) {
+      // the largest tiles run in whole rounds; smaller ones fill the gaps
+      const double rounds = s.slots == 256 && s.BM == 256 ? (double)((blocks + 255) / 256) : (double)blocks / s.slots;
+      cost = rounds * s.all > s.one ? rounds * s.all : s.one;
+    }
+    if (least == 0 || cost < least) {
+      least = cost;
+      best = s.kind;
+    }
+  }
+  return best;
+}
+
+// Blocks of row tiles of BM rows times panels of BN outputs, or 0 if there are too many.
+unsigned block_count(const I8Args& a, int BM, int BN, int* panels) {
+  *panels = (a.N + BN - 1) / BN;
+  const int64_t blocks = max_row_tiles(a.M, a.experts, a.offsets != nullptr, BM) * *panels;
+  return blocks > 0x7FFFFFFF ? 0 : (unsigned)blocks;
+}
+
+template <bool kF32>
+hipError_t launch_w8a8(const I8Args& a, W8a8 kind, hipStream_t st) {
+  int panels = 0;
+  unsigned blocks = 0;
+  auto grid = [&](int BM, int BN) { return (blocks = block_count(a, BM, BN, &panels)) != 0; };
+  switch (kind) {
+    case W8a8::kTile256:
+      if (grid(256, 256)) w8a8_tile_kernel<2, 4, 8, 1, kF32><<<blocks, 512, 0, st>>>(a, panels);
+      break;
+    case W8a8::kTile128:
+      if (grid(128, 128)) w8a8_tile_kernel<2, 2, 4, 2, kF32><<<blocks, 256, 0, st>>>(a, panels);
+      break;
+    case W8a8::kDeep128:
+      if (grid(128, 128)) w8a8_deep_kernel<2, 2, 4, 1, kF32><<<blocks, 256, 0, st>>>(a, panels);
+      break;
+    case W8a8::kDeep64x128:
+      if (grid(64, 128)) w8a8_deep_kernel<2, 2, 2, 1, kF32><<<blocks, 256, 0, st>>>(a, panels);
+      break;
+    case W8a8::kDeep64:
+      if (grid(64, 64)) w8a8_deep_kernel<2, 1, 2, 2, kF32><<<blocks, 256, 0, st>>>(a, panels);
+      break;
+    case W8a8::kStream32x64:
+      if (grid(32, 64)) w8a8_stream_kernel<2, 4, 4, false, kF32><<<blocks, 256, 0, st>>>(a);
+      break;
+    case W8a8::kStream16x64:
+      if (grid(16, 64)) w8a8_stream_kernel<1, 4, 4, false, kF32><<<blocks, 256, 0, st>>>(a);
+      break;
+    case W8a8::kRows16: {
+      // Two row blocks per wavefront once that leaves enough blocks, and K divided
+      // between two wavefronts where the row blocks alone fill the GPU, else four
+      // (one row: 2560 x 9216 6.6 us as one row block and four wavefronts, 9.0 as two
+      // and two; 9216 x 2560 6.6 and 6.4; 5120 x 17408 16.5 as two and four, 19.9 as
+      // one and four).
+      const int64_t nb = (a.N + kTileRows - 1) / kTileRows * (a.experts < a.M ? a.experts : a.M);
+      const bool past = (int64_t)a.experts * a.N * a.K >= (int64_t)64 << 20;  // larger than the caches keep
+      if (nb < 256) {
+        if (grid(16, 16)) w8a8_stream_kernel<1, 1, 4, false, kF32><<<blocks, 256, 0, st>>>(a);
+      } else if (nb < 512) {
+        if (!grid(16, 32)) break;
+        if (past) w8a8_stream_kernel<1, 2, 4, true, kF32><<<blocks, 256, 0, st>>>(a);
+        else w8a8_stream_kernel<1, 2, 4, false, kF32><<<blocks, 256, 0, st>>>(a);
+      } else {
+        if (!grid(16, 32)) break;
+        if (past) w8a8_stream_kernel<1, 2, 2, true, kF32><<<blocks, 128, 0, st>>>(a);
+        else w8a8_stream_kernel<1, 2, 2, false, kF32><<<blocks, 128, 0, st>>>(a);
+      }
+      break;
+    }
+  }
+  return blocks ? hipGetLastError() : hipErrorInvalidConfiguration;
 }
 
 }  // namespace
@@ -377,23 +693,8 @@ hipError_t launch_linear_w8a8(const int8_t* xq, const float* sx, int64_t M, int6
                               hipStream_t stream) {
   const I8Args a{xq, sx, offsets, q, d, y, (int)M, (int)K, (int)N, (int)experts,
                  (reinterpret_cast<uintptr_t>(y) | (uintptr_t)(N * (f32 ? 4 : 2))) % 16 == 0};
-  const int64_t nb = (N + kTileRows - 1) / kTileRows;
-  if (M > 64 * experts) {
-    const int64_t tiles = max_row_tiles(M, experts, offsets != nullptr, 256), panels = (nb + 15) / 16;
-    if (tiles * panels > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-    if (f32)
-      w8a8_tile_kernel<2, 4, 8, true><<<(unsigned)(tiles * panels), 512, 0, stream>>>(a, (int)panels);
-    else
-      w8a8_tile_kernel<2, 4, 8, false><<<(unsigned)(tiles * panels), 512, 0, stream>>>(a, (int)panels);
-    return hipGetLastError();
-  }
-  const int64_t blocks = max_row_tiles(M, experts, offsets != nullptr, 16) * nb;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  if (f32)
-    w8a8_stream_kernel<1, 1, 4, true><<<(unsigned)blocks, 256, 0, stream>>>(a);
-  else
-    w8a8_stream_kernel<1, 1, 4, false><<<(unsigned)blocks, 256, 0, stream>>>(a);
-  return hipGetLastError();
+  return f32 ? launch_w8a8<true>(a, choose_w8a8(M, N, K, experts), stream)
+             : launch_w8a8<false>(a, choose_w8a8(M, N, K, experts), stream);
 }
 
 }  // namespace w4
