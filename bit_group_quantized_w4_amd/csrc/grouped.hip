@@ -14,6 +14,8 @@
 #include "w4_launch.h"
 #include "w4_rows.h"
 
+#include <stdlib.h>
+
 namespace w4 {
 namespace {
 
@@ -108,12 +110,252 @@ __global__ __launch_bounds__(NW * 64) void grouped_stream_kernel(const GroupedAr
   }
 }
 
+// Tile form, for experts with many rows: a block of WM x WN wavefronts owns
+// BM = 16 WM TM rows of x and BN = 64 WN outputs, each wavefront TM x 4 tiles of
+// 16 x 16 outputs.  A step is one group of 128 inputs.
+//
+// x goes to LDS straight from memory, two steps ahead, in three buffers.  Lane l of
+// a load takes row l / 16 of four and its 16-byte chunk (l % 16) ^ (row % 16), so
+// that the sixteen rows of an operand are read without bank conflicts.  Codes go
+// straight to registers (each is used by two wavefronts only) and are widened
+// there.
+//
+// The partial sums of a group start from -1.5 * (sum of its x), which depends on the
+// row alone: each wavefront forms it for one row tile of the block with four MFMAs
+// against a constant operand, a step ahead, and shares it through LDS; the first
+// MFMA of every chain takes it as its third operand.  Per step and wavefront that is
+// 4 MFMAs beside 16 TM.
+//
+// The four output tiles j of a step follow each other; beside the products of one
+// run the scaled accumulation of the one before, the widening of the next one's
+// codes and the loads.  The barrier of a step stands before the last tile's products
+// of the group before: beside these the operands of the new group are read.
+//
+// Steps past the last group (there are up to two, for the three buffers) read zeros
+// without touching memory.
+template <int WM, int WN, int TM, bool S16, bool kF32>
+__global__ __launch_bounds__(WM* WN * 64, 2) void grouped_tile_kernel(const GroupedArgs a, int panels) {
+  constexpr int TN = 4, NW = WM * WN, BM = 16 * WM * TM, BN = 16 * WN * TN;
+  constexpr int LA = BM / 4 / NW;  // 1 KiB loads of x per wavefront and step
+  static_assert(LA * NW * 4 == BM && LA <= 4 && 4 % LA == 0, "loads of x shared out evenly, within 16 rows");
+  __shared__ __attribute__((aligned(1024))) uint8_t x0[BM * 256], x1[BM * 256], x2[BM * 256];
+  __shared__ __attribute__((aligned(1024))) float off0[BM], off1[BM], off2[BM];
+
+  // (offsets whose ranges overlap could make more tiles than the launch covers)
+  const int tiles = min(count_row_tiles(a.offsets, a.experts, a.M, BM), (int)gridDim.x / panels);
+  if ((int)blockIdx.x >= tiles * panels) return;
+  int t, p;
+  tile_of_block(blockIdx.x, tiles, panels, t, p);
+  RowTile rt;
+  if (!find_row_tile(a.offsets, a.experts, a.M, BM, t, rt)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nl = lane & 15, kb = lane >> 4;
+  const int wm = wave / WN, wn = wave - wm * WN;
+  const int K = a.K, G = K / kGroup, Q = (G + 3) >> 2, GP = 4 * Q;
+  const int nb = (a.N + kTileRows - 1) / kTileRows, rb0 = p * (BN / 16) + wn * TN;
+  const int rows = rt.r1 - rt.r0;
+
+  constexpr uint32_t kScale = S16 ? 2u : 4u;
+  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.x + (int64_t)rt.r0 * K, (uint32_t)rows * (uint32_t)K * 2u);
+  const __amdgpu_buffer_rsrc_t rq = make_rsrc(a.q + (int64_t)rt.expert * nb * GP * 1024, (uint32_t)nb * GP * 1024u);
+  const __amdgpu_buffer_rsrc_t rd = make_rsrc(static_cast<const uint8_t*>(a.d) + (int64_t)rt.expert * nb * GP * 16 * kScale,
+                                              (uint32_t)nb * GP * 16u * kScale);
+  uint32_t xo = (uint32_t)(4 * wave * LA + kb) * (uint32_t)K * 2u + 16u * (nl ^ ((4 * wave * LA + kb) & 15));
+  const uint32_t qo = (uint32_t)rb0 * GP * 1024u + 16u * lane;
+  const uint32_t so = ((uint32_t)rb0 * Q * 16u + nl) * 4u * kScale;
+  typedef __attribute__((address_space(3))) void* lds_ptr;
+  auto load_x = [&](int i, int g, uint8_t* to) {
+    // rows 4 (wave LA + i) ..: 4 i of them further than xo, chunks exchanged by the same 4 i
+    const uint32_t k = g < G ? (uint32_t)g * 256u : kOob;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_ptr)(to + (wave * LA + i) * 1024), 16,
+                                             (int)((xo ^ (64u * i)) + (uint32_t)(8 * i * K) + k), 0, 0, 0);
+  };
+  uint4 w[TN];
+  float d[TN];      // scales of the group in work
+  uint32_t dn[TN];  // of the next, as loaded
+  auto load_w = [&](int j, int g) {
+    const uint32_t k = g < G ? (uint32_t)g * 1024u : kOob;
+    w[j] = bload<0>(rq, qo + (uint32_t)(j * GP) * 1024u + k);
+  };
+  auto load_d = [&](int j, int g) {
+    const uint32_t k = g < G ? ((uint32_t)(g >> 2) * 64u + (uint32_t)(g & 3)) * kScale : kOob;
+    const int o = (int)(so + (uint32_t)(j * Q) * 64u * kScale + k);
+    if constexpr (S16)
+      dn[j] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rd, o, 0, 0);
+    else
+      dn[j] = __builtin_amdgcn_raw_buffer_load_b32(rd, o, 0, 0);
+  };
+
+  f32x4 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  bf16x8 x[TM][4], b[4];
+  f32x4 off[TM], c[2][TM];
+  uint32_t xa = (uint32_t)(wm * TM * 16 + nl) * 256u + 16u * (kb ^ nl);
+  const UnpackConsts uc = unpack_consts();
+  const bf16x8 kneg = bitcast<bf16x8>(u32x4{kNeg15x2, kNeg15x2, kNeg15x2, kNeg15x2});
+
+  auto read_x = [&](int i, const uint8_t* from) {  // the four inputs-octets of 32-input step i
+#pragma unroll
+    for (int m = 0; m < TM; ++m) x[m][i] = *reinterpret_cast<const bf16x8*>(from + (xa ^ (64u * i)) + m * 4096);
+  };
+  auto widen = [&](int i, int j) {
+    const uint32_t wj = i == 0 ? w[j].x : i == 1 ? w[j].y : i == 2 ? w[j].z : w[j].w;
+    uint32_t u[4];
+    unpack_word(wj, u, uc);
+    b[i] = bitcast<bf16x8>(u32x4{u[0], u[1], u[2], u[3]});
+  };
+  // acc += d c for row tile m of output tile j, c in buffer s
+  auto accumulate = [&](int s, int m, int j, float dj) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[m][j][e] = fmaf(dj, c[s][m][e], acc[m][j][e]);
+  };
+  // 32-input step i of output tile j's products into buffer s
+  auto multiply = [&](int s, int i) {
+#pragma unroll
+    for (int m = 0; m < TM; ++m) c[s][m] = mfma16x16x32(x[m][i], b[i], i == 0 ? off[m] : c[s][m]);
+  };
+  // -1.5 * sum of x over the group in `from`, for one row tile of the block
+  const uint32_t tile = (uint32_t)(wm * TM + wn % TM);
+  bf16x8 xt[4];
+  auto read_tile = [&](const uint8_t* from) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) xt[i] = *reinterpret_cast<const bf16x8*>(from + ((xa ^ (64u * i)) + (uint32_t)(wn % TM) * 4096u));
+  };
+  auto write_off = [&](float* to) {
+    f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v = mfma16x16x32(xt[i], kneg, v);
+    // every column holds the same sums: lanes of one quarter write the same bytes
+    *reinterpret_cast<f32x4*>(to + tile * 16u + 4u * kb) = v;
+  };
+  auto read_off = [&](const float* from) {
+#pragma unroll
+    for (int m = 0; m < TM; ++m) off[m] = *reinterpret_cast<const f32x4*>(from + (wm * TM + m) * 16 + 4 * kb);
+  };
+#define W4_FENCE __builtin_amdgcn_sched_barrier(0)
+  // Group g: x in `cur`, its start values in `ocur`; the next group's x in `nxt`,
+  // its start values go to `onxt`; the one after that is loaded into `far`.
+  auto step = [&](int g, const uint8_t* cur, const uint8_t* nxt, uint8_t* far, const float* ocur, float* onxt) {
+    asm volatile("" ::: "memory");
+    // the x of the next group has landed: only the 2 TN loads of codes and scales
+    // issued after it may be outstanding
+    __builtin_amdgcn_s_waitcnt(0x0070 | (2 * TN));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    // the addresses derived from these are cheaper formed anew than kept (256 VGPRs)
+    asm volatile("" : "+v"(xa), "+v"(xo));
+    W4_FENCE;
+    // last output tile of the group before
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      multiply(1, i);
+      W4_FENCE;
+      read_x(i, cur);
+      if (i < LA) load_x(i, g + 2, far);
+      if (i < TM) accumulate(0, i, 2, d[2]);
+      widen(i, 0);
+      W4_FENCE;
+    }
+    read_off(ocur);
+    const float d3 = d[3];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) d[j] = __uint_as_float(S16 ? dn[j] << 16 : dn[j]);
+    W4_FENCE;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        multiply(j & 1, i);
+        W4_FENCE;
+        if (i < TM) accumulate((j & 1) ^ 1, i, (j + 3) & 3, j == 0 ? d3 : d[j - 1]);
+        widen(i, j + 1);
+        if (j == 0) load_d(i, g + 1);
+        if (i == 3) load_w(j, g + 1);
+        if (i == 0 && j == 1) read_tile(nxt);
+        if (i == 1 && j == 2) write_off(onxt);
+        W4_FENCE;
+      }
+    }
+    load_w(3, g + 1);
+    W4_FENCE;
+  };
+
+  // before the first group: products of zeros stand in for the group before it
+#pragma unroll
+  for (int i = 0; i < LA; ++i) load_x(i, 0, x0);
+#pragma unroll
+  for (int i = 0; i < LA; ++i) load_x(i, 1, x1);
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    load_w(j, 0);
+    load_d(j, 0);
+    d[j] = 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    b[i] = bitcast<bf16x8>(u32x4{0, 0, 0, 0});
+#pragma unroll
+    for (int m = 0; m < TM; ++m) x[m][i] = bitcast<bf16x8>(u32x4{0, 0, 0, 0});
+  }
+#pragma unroll
+  for (int m = 0; m < TM; ++m) off[m] = c[0][m] = c[1][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  read_tile(x0);
+  write_off(off0);
+  for (int g = 0; g < G; g += 3) {
+    step(g, x0, x1, x2, off0, off1);
+    step(g + 1, x1, x2, x0, off1, off2);
+    step(g + 2, x2, x0, x1, off2, off0);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) multiply(1, i);
+#pragma unroll
+  for (int m = 0; m < TM; ++m) {
+    accumulate(0, m, 2, d[2]);
+    accumulate(1, m, 3, d[3]);
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load into LDS outlives the block
+#undef W4_FENCE
+
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const int n = (rb0 + j) * kTileRows + nl;
+    if (n >= a.N) continue;
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = rt.r0 + 16 * (wm * TM + m) + 4 * kb + e;
+        if (r < rt.r1) store_out<kF32>(a, r, n, 16.0f * acc[m][j][e]);
+      }
+  }
+}
+
 }  // namespace
 
 hipError_t launch_linear_grouped(const uint16_t* x, int64_t M, int64_t K, const int32_t* offsets, int64_t experts,
                                  const uint8_t* q, const void* d, bool s16, int64_t N, void* y, bool f32,
                                  hipStream_t stream) {
   const GroupedArgs a{x, offsets, q, d, y, (int)M, (int)K, (int)N, (int)experts};
+  const char* ge = getenv("GCFG");
+  const int cfg = ge ? atoi(ge) : M > 32 * experts ? 1 : 0;
+#define GC(c, WM, WN, TM) \
+  if (cfg == c) { \
+    const int64_t panels = (N + 64 * WN - 1) / (64 * WN), bl = max_row_tiles(M, experts, true, 16 * WM * TM) * panels; \
+    if (bl > 0x7FFFFFFF) return hipErrorInvalidConfiguration; \
+    if (s16 && f32) grouped_tile_kernel<WM, WN, TM, true, true><<<(unsigned)bl, WM * WN * 64, 0, stream>>>(a, (int)panels); \
+    else if (s16) grouped_tile_kernel<WM, WN, TM, true, false><<<(unsigned)bl, WM * WN * 64, 0, stream>>>(a, (int)panels); \
+    else if (f32) grouped_tile_kernel<WM, WN, TM, false, true><<<(unsigned)bl, WM * WN * 64, 0, stream>>>(a, (int)panels); \
+    else grouped_tile_kernel<WM, WN, TM, false, false><<<(unsigned)bl, WM * WN * 64, 0, stream>>>(a, (int)panels); \
+    return hipGetLastError(); \
+  }
+  GC(1, 2, 4, 4) GC(2, 2, 4, 2) GC(3, 1, 4, 4)
   const int64_t blocks = max_row_tiles(M, experts, true, 16) * ((N + kTileRows - 1) / kTileRows);
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   const unsigned nblk = (unsigned)blocks;
