@@ -171,6 +171,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_tile_kernel(const Grou
                                              (int)((xo ^ (64u * i)) + (uint32_t)(8 * i * K) + k), 0, 0, 0);
   };
   uint4 w[TN];
+  uint32_t word3 = 0;  // the last word of tile 3, widened after its registers are loaded anew
   float d[TN];      // scales of the group in work
   uint32_t dn[TN];  // of the next, as loaded
   auto load_w = [&](int j, int g) {
@@ -201,21 +202,30 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_tile_kernel(const Grou
 #pragma unroll
     for (int m = 0; m < TM; ++m) x[m][i] = *reinterpret_cast<const bf16x8*>(from + (xa ^ (64u * i)) + m * 4096);
   };
-  auto widen = [&](int i, int j) {
-    const uint32_t wj = i == 0 ? w[j].x : i == 1 ? w[j].y : i == 2 ? w[j].z : w[j].w;
-    uint32_t u[4];
-    unpack_word(wj, u, uc);
-    b[i] = bitcast<bf16x8>(u32x4{u[0], u[1], u[2], u[3]});
+  // Word i of a tile's codes as its four pairs of bf16, pair q at a time.
+  auto widen = [&](int i, uint32_t word, int q) {
+    u32x4 v = bitcast<u32x4>(b[i]);
+    v[q] = ((q == 0 ? word : rotr32(word, 4 * q)) & uc.mask) | uc.magic;
+    b[i] = bitcast<bf16x8>(v);
   };
-  // acc += d c for row tile m of output tile j, c in buffer s
-  auto accumulate = [&](int s, int m, int j, float dj) {
+  auto word_of = [&](int i, int j) { return i == 0 ? w[j].x : i == 1 ? w[j].y : i == 2 ? w[j].z : w[j].w; };
+  // 32-input step i of an output tile's products into buffer s.  An MFMA occupies
+  // the matrix unit for as long as four vector instructions take: after each come
+  // its share of row tile i's accumulation acc += da c for the tile before (ja, in the
+  // other buffer) and of the widening of one word into b[(i + 3) & 3], whose last
+  // use the step before was.
+  auto multiply = [&](int s, int i, int ja, float da, uint32_t word) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[m][j][e] = fmaf(dj, c[s][m][e], acc[m][j][e]);
-  };
-  // 32-input step i of output tile j's products into buffer s
-  auto multiply = [&](int s, int i) {
+    for (int m = 0; m < TM; ++m) {
+      c[s][m] = mfma16x16x32(x[m][i], b[i], i == 0 ? off[m] : c[s][m]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int m = 0; m < TM; ++m) c[s][m] = mfma16x16x32(x[m][i], b[i], i == 0 ? off[m] : c[s][m]);
+      for (int e = m * 4 / TM; e < (m + 1) * 4 / TM; ++e) {
+        if (i < TM) acc[i][ja][e] = fmaf(da, c[s ^ 1][i][e], acc[i][ja][e]);
+        widen((i + 3) & 3, word, e);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
   // -1.5 * sum of x over the group in `from`, for one row tile of the block
   const uint32_t tile = (uint32_t)(wm * TM + wn % TM);
@@ -251,12 +261,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_tile_kernel(const Grou
     // last output tile of the group before
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      multiply(1, i);
-      W4_FENCE;
+      multiply(1, i, 2, d[2], i == 0 ? word3 : word_of(i - 1, 0));
       read_x(i, cur);
       if (i < LA) load_x(i, g + 2, far);
-      if (i < TM) accumulate(0, i, 2, d[2]);
-      widen(i, 0);
       W4_FENCE;
     }
     read_off(ocur);
@@ -268,17 +275,15 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_tile_kernel(const Grou
     for (int j = 0; j < 3; ++j) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        multiply(j & 1, i);
-        W4_FENCE;
-        if (i < TM) accumulate((j & 1) ^ 1, i, (j + 3) & 3, j == 0 ? d3 : d[j - 1]);
-        widen(i, j + 1);
+        multiply(j & 1, i, (j + 3) & 3, j == 0 ? d3 : d[j - 1], i == 0 ? word_of(3, j) : word_of(i - 1, j + 1));
         if (j == 0) load_d(i, g + 1);
-        if (i == 3) load_w(j, g + 1);
+        if (i == 1) load_w(j, g + 1);  // its last word was widened beside step 0
         if (i == 0 && j == 1) read_tile(nxt);
         if (i == 1 && j == 2) write_off(onxt);
         W4_FENCE;
       }
     }
+    word3 = w[3].w;
     load_w(3, g + 1);
     W4_FENCE;
   };
@@ -314,25 +319,38 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_tile_kernel(const Grou
     step(g + 2, x2, x0, x1, off2, off0);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) multiply(1, i);
+  for (int i = 0; i < 4; ++i) multiply(1, i, 2, d[2], word3);  // (only step 3's word is still to be widened)
 #pragma unroll
-  for (int m = 0; m < TM; ++m) {
-    accumulate(0, m, 2, d[2]);
-    accumulate(1, m, 3, d[3]);
-  }
+  for (int m = 0; m < TM; ++m)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[m][3][e] = fmaf(d[3], c[1][m][e], acc[m][3][e]);
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load into LDS outlives the block
 #undef W4_FENCE
 
+  // Stores past the tile's last row or the matrix's last output lie outside the
+  // buffer and are dropped (the launch keeps a tile's rows of y below 2 GiB).
+  constexpr uint32_t kOut = kF32 ? 4u : 2u;
+  const __amdgpu_buffer_rsrc_t ry = make_rsrc(static_cast<uint8_t*>(a.y) + (int64_t)rt.r0 * a.N * kOut,
+                                              (uint32_t)rows * (uint32_t)a.N * kOut);
+  const uint32_t pitch = (uint32_t)a.N * kOut;
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
     const int n = (rb0 + j) * kTileRows + nl;
-    if (n >= a.N) continue;
+    const uint32_t at = n < a.N ? (uint32_t)(16 * wm * TM + 4 * kb) * pitch + (uint32_t)n * kOut : kOob;
 #pragma unroll
     for (int m = 0; m < TM; ++m)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = rt.r0 + 16 * (wm * TM + m) + 4 * kb + e;
-        if (r < rt.r1) store_out<kF32>(a, r, n, 16.0f * acc[m][j][e]);
+      for (int e = 0; e < 4; e += 2) {
+        const uint32_t o = at + (uint32_t)(16 * m + e) * pitch;
+        const float v0 = 16.0f * acc[m][j][e], v1 = 16.0f * acc[m][j][e + 1];
+        if constexpr (kF32) {
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v0), ry, (int)o, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v1), ry, (int)(o + pitch), 0, 0);
+        } else {
+          const uint32_t v = f32x2_to_bf16x2(v0, v1);
+          __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v, ry, (int)o, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v >> 16), ry, (int)(o + pitch), 0, 0);
+        }
       }
   }
 }

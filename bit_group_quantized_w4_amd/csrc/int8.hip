@@ -157,7 +157,7 @@ __device__ __forceinline__ void store_tile(const I8Args& a, const RowTile& rt, i
         uint32_t u[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          u[e] = (uint32_t)f32_to_bf16_rne(v[2 * e]) | (uint32_t)f32_to_bf16_rne(v[2 * e + 1]) << 16;
+          u[e] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
         *reinterpret_cast<uint4*>(y) = make_uint4(u[0], u[1], u[2], u[3]);
         *reinterpret_cast<uint4*>(y + 8) = make_uint4(u[4], u[5], u[6], u[7]);
       } else {

@@ -90,6 +90,12 @@ __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
   return (uint16_t)(u >> 16);
 }
 
+// Two fp32 -> two bf16 in one instruction, the same rounding (lo in the low half).
+__device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
+  const bf16x2 v = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
 template <typename T, typename S>
 __device__ __forceinline__ T bitcast(const S& s) {
   static_assert(sizeof(T) == sizeof(S), "size mismatch");
