@@ -14,8 +14,6 @@
 #include "w4_launch.h"
 #include "w4_rows.h"
 
-#include <stdlib.h>
-
 namespace w4 {
 namespace {
 
@@ -44,69 +42,111 @@ __device__ __forceinline__ f32x4 mfma16x16x32(const bf16x8& a, const bf16x8& b, 
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-template <bool S16>
-__device__ __forceinline__ float load_scale(const void* d, int64_t i) {
-  if constexpr (S16)
-    return __uint_as_float((uint32_t) static_cast<const uint16_t*>(d)[i] << 16);
-  else
-    return static_cast<const float*>(d)[i];
-}
-
-// A block owns one 16-output row block and a tile of 16 rows of x; its NW
-// wavefronts divide the groups.
-template <int NW, bool S16, bool kF32>
+// Streaming form, for experts with few rows: a block owns R row blocks of 16
+// outputs and a tile of 16 rows of x; its NW wavefronts divide the groups.  Each
+// wavefront keeps D groups of codes, scales and x in flight, straight from memory;
+// a group past its last reads zeros without touching memory, so that every load is
+// unconditional.  Codes are read through the caches, since an expert with more than
+// 16 rows is read by several blocks.  Bound by the latency of a few dependent loads
+// (offsets, then codes): two tokens of two experts of 64, 2048 x 2560 each, 10.9 us for
+// 44.7 MB (4.1 TB/s); three or four groups in flight, and past the caches, took 12.7
+// and 14.0 us.
+template <int R, int NW, bool S16, bool kF32>
 __global__ __launch_bounds__(NW * 64) void grouped_stream_kernel(const GroupedArgs a) {
-  const int nb = (a.N + kTileRows - 1) / kTileRows;
-  const int t = blockIdx.x / nb, rb = blockIdx.x - t * nb;
+  constexpr int D = 2;
+  const int nb = (a.N + kTileRows - 1) / kTileRows, panels = (nb + R - 1) / R;
+  const int t = blockIdx.x / panels, rb0 = (blockIdx.x - t * panels) * R;
   RowTile rt;
   if (!find_row_tile(a.offsets, a.experts, a.M, 16, t, rt)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nl = lane & 15, kb = lane >> 4;
   const int G = a.K / kGroup, Q = (G + 3) >> 2, GP = 4 * Q;
   const int g0 = (int)((int64_t)G * wave / NW), g1 = (int)((int64_t)G * (wave + 1) / NW);
-  const uint4* q = reinterpret_cast<const uint4*>(a.q) + ((int64_t)rt.expert * nb + rb) * GP * kTileLanes + lane;
-  const int64_t s0 = (((int64_t)rt.expert * nb + rb) * Q * kTileRows + nl) * 4;
+  constexpr uint32_t kScale = S16 ? 2u : 4u;
   const __amdgpu_buffer_rsrc_t rx =
       make_rsrc(a.x + (int64_t)rt.r0 * a.K, (uint32_t)(rt.r1 - rt.r0) * (uint32_t)a.K * 2u);
-  const uint32_t xo = nl < rt.r1 - rt.r0 ? ((uint32_t)nl * a.K + 8u * kb) * 2u : kOob;
+  const __amdgpu_buffer_rsrc_t rq = make_rsrc(a.q + (int64_t)rt.expert * nb * GP * 1024, (uint32_t)nb * GP * 1024u);
+  const __amdgpu_buffer_rsrc_t rd = make_rsrc(static_cast<const uint8_t*>(a.d) + (int64_t)rt.expert * nb * GP * 16 * kScale,
+                                              (uint32_t)nb * GP * 16u * kScale);
+  // (row blocks past the last one lie outside the buffers, as rows of x past the tile's last do)
+  const uint32_t xo = ((uint32_t)nl * a.K + 8u * kb) * 2u, qo = (uint32_t)rb0 * GP * 1024u + 16u * lane,
+                 so = ((uint32_t)rb0 * Q * 16u + nl) * 4u * kScale;
+  uint4 x[D][4], w[D][R];
+  uint32_t d[D][R];
+  auto issue = [&](int c, int g) {
+    const bool in = g < g1;
+    const uint32_t kx = in ? (uint32_t)g * 256u : kOob, kq = in ? (uint32_t)g * 1024u : kOob;
+    const uint32_t kd = in ? ((uint32_t)(g >> 2) * 64u + (uint32_t)(g & 3)) * kScale : kOob;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      w[c][r] = bload<0>(rq, qo + (uint32_t)(r * GP) * 1024u + kq);
+      const int o = (int)(so + (uint32_t)(r * Q) * 64u * kScale + kd);
+      if constexpr (S16)
+        d[c][r] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rd, o, 0, 0);
+      else
+        d[c][r] = __builtin_amdgcn_raw_buffer_load_b32(rd, o, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[c][i] = bload<0>(rx, xo + 64u * i + kx);
+  };
   const UnpackConsts uc = unpack_consts();
   const bf16x8 kneg = bitcast<bf16x8>(u32x4{kNeg15x2, kNeg15x2, kNeg15x2, kNeg15x2});
 
-  f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int g = g0; g < g1; ++g) {
-    const uint4 w = q[(int64_t)g * kTileLanes];
-    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-    f32x4 c = f32x4{0.f, 0.f, 0.f, 0.f};
-    bf16x8 x[4];
+  f32x4 acc[R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = bitcast<bf16x8>(bload<0>(rx, xo + (uint32_t)g * 256u + 64u * i));
-      c = mfma16x16x32(x[i], kneg, c);
+  for (int r = 0; r < R; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < D; ++c) {
+    issue(c, g0 + c);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  for (int g = g0; g < g1; g += D) {
+#pragma unroll
+    for (int c = 0; c < D; ++c) {
+      f32x4 off = f32x4{0.f, 0.f, 0.f, 0.f}, v[R];
+      float dr[R];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) off = mfma16x16x32(bitcast<bf16x8>(x[c][i]), kneg, off);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        v[r] = off;
+        dr[r] = __uint_as_float(S16 ? d[c][r] << 16 : d[c][r]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint32_t word = i == 0 ? w[c][r].x : i == 1 ? w[c][r].y : i == 2 ? w[c][r].z : w[c][r].w;
+          uint32_t b[4];
+          unpack_word(word, b, uc);
+          v[r] = mfma16x16x32(bitcast<bf16x8>(x[c][i]), bitcast<bf16x8>(u32x4{b[0], b[1], b[2], b[3]}), v[r]);
+        }
+      issue(c, g + c + D);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[r][e] = fmaf(dr[r], v[r][e], acc[r][e]);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t b[4];
-      unpack_word(words[i], b, uc);
-      c = mfma16x16x32(x[i], bitcast<bf16x8>(u32x4{b[0], b[1], b[2], b[3]}), c);
-    }
-    const float d = load_scale<S16>(a.d, s0 + (int64_t)(g >> 2) * kTileRows * 4 + (g & 3));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = fmaf(d, c[j], acc[j]);
   }
 
-  __shared__ f32x4 red[NW][64];
-  red[wave][lane] = acc;
+  __shared__ f32x4 red[NW][R][64];
+#pragma unroll
+  for (int r = 0; r < R; ++r) red[wave][r][lane] = acc[r];
   __syncthreads();
-  const int n = rb * kTileRows + nl;
-  if (wave != 0 || n >= a.N) return;
+  for (int r = wave; r < R; r += NW) {
+    const int n = (rb0 + r) * kTileRows + nl;
+    if (n >= a.N) continue;
+    f32x4 v = red[0][r][lane];
 #pragma unroll
-  for (int w = 1; w < NW; ++w)
+    for (int u = 1; u < NW; ++u)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] += red[w][lane][j];
+      for (int e = 0; e < 4; ++e) v[e] += red[u][r][lane][e];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int m = rt.r0 + 4 * kb + j;
-    if (m < rt.r1) store_out<kF32>(a, m, n, 16.0f * acc[j]);
+    for (int e = 0; e < 4; ++e) {
+      const int m = rt.r0 + 4 * kb + e;
+      if (m < rt.r1) store_out<kF32>(a, m, n, 16.0f * v[e]);
+    }
   }
 }
 
@@ -130,6 +170,12 @@ __global__ __launch_bounds__(NW * 64) void grouped_stream_kernel(const GroupedAr
 // run the scaled accumulation of the one before, the widening of the next one's
 // codes and the loads.  The barrier of a step stands before the last tile's products
 // of the group before: beside these the operands of the new group are read.
+//
+// 8190 rows of eight experts, 9216 x 2560: 398 us (972 TFLOP/s).  Bound by the issue of
+// vector instructions: an MFMA takes about nine of its sixteen cycles to issue and
+// each vector instruction four more, of which there are 2.9 per MFMA (widening 1.75,
+// accumulation 1).  64 rows per block (two blocks of four wavefronts per CU, whose
+// barriers do not wait for each other) beat 128 rows in one block of eight (437 us).
 //
 // Steps past the last group (there are up to two, for the three buffers) read zeros
 // without touching memory.
@@ -263,7 +309,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_tile_kernel(const Grou
     for (int i = 0; i < 4; ++i) {
       multiply(1, i, 2, d[2], i == 0 ? word3 : word_of(i - 1, 0));
       read_x(i, cur);
-      if (i < LA) load_x(i, g + 2, far);
+#pragma unroll
+      for (int l = i * LA / 4; l < (i + 1) * LA / 4; ++l) load_x(l, g + 2, far);
       W4_FENCE;
     }
     read_off(ocur);
@@ -328,7 +375,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_tile_kernel(const Grou
 #undef W4_FENCE
 
   // Stores past the tile's last row or the matrix's last output lie outside the
-  // buffer and are dropped (the launch keeps a tile's rows of y below 2 GiB).
+  // buffer and are dropped.  (Codes below 2 GiB keep N below 2^23, and the 64 rows of
+  // y below 2 GiB.)
+  static_assert(BM <= 64, "offsets into the rows of y below kOob");
   constexpr uint32_t kOut = kF32 ? 4u : 2u;
   const __amdgpu_buffer_rsrc_t ry = make_rsrc(static_cast<uint8_t*>(a.y) + (int64_t)rt.r0 * a.N * kOut,
                                               (uint32_t)rows * (uint32_t)a.N * kOut);
@@ -355,33 +404,41 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_tile_kernel(const Grou
   }
 }
 
+// The kernel goes by the average rows of an expert that has any (the true sizes are on
+// the GPU).  Up to 8 the weight stream is all there is to do: four row blocks per
+// wavefront once they leave 640 blocks or more, else two (32 rows of 64 experts of
+// 1408 x 2560: 15.6 us either way; 64 rows of eight of 9216 x 2560: 26.5 against 28.9;
+// 16 rows of eight of 2560 x 9216: two, 26.6 against 36).  Up to 64, tiles of 32 rows
+// (256 rows of 16 experts of 5120 x 2560: 34.8 us, 38.0 streamed, 43.3 as 64 rows; 4096
+// rows of 64 of 1408 x 2560: 71.4 and 81.3); beyond, 64 rows (1024 rows of eight of
+// 9216 x 2560: 75.6 us, 86.0 as 32 rows).
+template <bool S16, bool kF32>
+hipError_t launch_grouped(const GroupedArgs& a, hipStream_t st) {
+  const int64_t busy = a.experts < a.M ? a.experts : a.M, rows = (a.M + busy - 1) / busy;
+  const int64_t nb = (a.N + kTileRows - 1) / kTileRows;
+  const bool four = busy * nb >= 2560;
+  const int BM = rows <= 8 ? 16 : rows <= 64 ? 32 : 64, BN = rows > 8 ? 256 : four ? 64 : 32;
+  const int64_t panels = (a.N + BN - 1) / BN, blocks = max_row_tiles(a.M, a.experts, true, BM) * panels;
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const unsigned n = (unsigned)blocks;
+  if (rows > 64) grouped_tile_kernel<1, 4, 4, S16, kF32><<<n, 256, 0, st>>>(a, (int)panels);
+  else if (rows > 8) grouped_tile_kernel<1, 4, 2, S16, kF32><<<n, 256, 0, st>>>(a, (int)panels);
+  else if (four) grouped_stream_kernel<4, 2, S16, kF32><<<n, 128, 0, st>>>(a);
+  else grouped_stream_kernel<2, 2, S16, kF32><<<n, 128, 0, st>>>(a);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_linear_grouped(const uint16_t* x, int64_t M, int64_t K, const int32_t* offsets, int64_t experts,
                                  const uint8_t* q, const void* d, bool s16, int64_t N, void* y, bool f32,
                                  hipStream_t stream) {
   const GroupedArgs a{x, offsets, q, d, y, (int)M, (int)K, (int)N, (int)experts};
-  const char* ge = getenv("GCFG");
-  const int cfg = ge ? atoi(ge) : M > 32 * experts ? 1 : 0;
-#define GC(c, WM, WN, TM) \
-  if (cfg == c) { \
-    const int64_t panels = (N + 64 * WN - 1) / (64 * WN), bl = max_row_tiles(M, experts, true, 16 * WM * TM) * panels; \
-    if (bl > 0x7FFFFFFF) return hipErrorInvalidConfiguration; \
-    if (s16 && f32) grouped_tile_kernel<WM, WN, TM, true, true><<<(unsigned)bl, WM * WN * 64, 0, stream>>>(a, (int)panels); \
-    else if (s16) grouped_tile_kernel<WM, WN, TM, true, false><<<(unsigned)bl, WM * WN * 64, 0, stream>>>(a, (int)panels); \
-    else if (f32) grouped_tile_kernel<WM, WN, TM, false, true><<<(unsigned)bl, WM * WN * 64, 0, stream>>>(a, (int)panels); \
-    else grouped_tile_kernel<WM, WN, TM, false, false><<<(unsigned)bl, WM * WN * 64, 0, stream>>>(a, (int)panels); \
-    return hipGetLastError(); \
-  }
-  GC(1, 2, 4, 4) GC(2, 2, 4, 2) GC(3, 1, 4, 4)
-  const int64_t blocks = max_row_tiles(M, experts, true, 16) * ((N + kTileRows - 1) / kTileRows);
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  const unsigned nblk = (unsigned)blocks;
-  if (s16 && f32) grouped_stream_kernel<4, true, true><<<nblk, 256, 0, stream>>>(a);
-  else if (s16) grouped_stream_kernel<4, true, false><<<nblk, 256, 0, stream>>>(a);
-  else if (f32) grouped_stream_kernel<4, false, true><<<nblk, 256, 0, stream>>>(a);
-  else grouped_stream_kernel<4, false, false><<<nblk, 256, 0, stream>>>(a);
-  return hipGetLastError();
+  const int kind = (s16 ? 2 : 0) | (f32 ? 1 : 0);
+  return kind == 0   ? launch_grouped<false, false>(a, stream)
+         : kind == 1 ? launch_grouped<false, true>(a, stream)
+         : kind == 2 ? launch_grouped<true, false>(a, stream)
+                     : launch_grouped<true, true>(a, stream);
 }
 
 }  // namespace w4
