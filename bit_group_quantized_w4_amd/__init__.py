@@ -581,49 +581,74 @@ def dense_linear_f32(x, W, out=None):
 # 8-bit integers with token and channel scales; rows sorted by expert
 # ----------------------------------------------------------------------------
 
-def _launch(name, device, *args):
-    """Call `name` with the current stream of `device`, made current for the launch
+# The handle of a device's current stream, as an integer (a Stream object costs as much
+# to make as a launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_gpu = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _launch(name, index, *args):
+    """Call `name` with the current stream of GPU `index`, made current for the launch
     (a null stream is the current device's)."""
-    fn = getattr(_lib, name)
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _launch(name, device, *args)
-    _check(fn(*args, ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)), name)
+    if index != _current_gpu():
+        with torch.cuda.device(index):
+            return _launch(name, index, *args)
+    status = getattr(_lib, name)(*args, _raw_stream(index))
+    if status:
+        _check(status, name)
 
 
-def _sized(t, dtype, shape, name):
-    """_dev with the shape checked: the kernels take sizes from other arguments."""
-    p = _dev(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    return p
-
-
-def _elements(t, dtype, count, name):
-    p = _dev(t, dtype, name)
-    if t.numel() != count:
-        raise ValueError(f"{name} must hold {count} elements (got {t.numel()})")
-    return p
-
-
-def _matrix(t, name):
+def _first(t, dtypes, name):
+    """The first tensor of a call: its GPU is the call's.  Returns (GPU index, shape)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 2:
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))} (got {t.dtype})")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.get_device(), t.shape
+
+
+def _rows(t, dtypes, name):
+    """_first of a matrix: (GPU index, rows, columns)."""
+    if isinstance(t, torch.Tensor) and t.dim() != 2:
         raise ValueError(f"{name} must be 2-D (got shape {tuple(t.shape)})")
-    return t.shape
+    dev, shape = _first(t, dtypes, name)
+    return dev, shape[0], shape[1]
+
+
+def _ptr(t, dtype, index, name, shape=None, count=None):
+    """Address of another tensor of a call on GPU `index`, its type, shape or number of
+    elements checked: the kernels take sizes from other arguments."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.get_device() != index:
+        raise ValueError(f"{name}: tensors on several devices ({t.device} and cuda:{index})")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if count is not None and t.numel() != count:
+        raise ValueError(f"{name} must hold {count} elements (got {t.numel()})")
+    return t.data_ptr()
 
 
 def _output(out, out_dtype, M, N, device):
     """(y, whether it is fp32) of a product's `out` and `out_dtype` arguments."""
-    if out is not None:
-        if not isinstance(out, torch.Tensor):
-            raise TypeError("out must be a torch.Tensor")
-        out_dtype = out.dtype
-    if out_dtype not in OUT_DTYPES:
-        raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
-    y = out if out is not None else torch.empty((M, N), dtype=out_dtype, device=device)
-    return y, out_dtype == torch.float32
+    if out is None:
+        if out_dtype not in OUT_DTYPES:
+            raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+        return torch.empty((M, N), dtype=out_dtype, device=device), out_dtype == torch.float32
+    if not isinstance(out, torch.Tensor):
+        raise TypeError("out must be a torch.Tensor")
+    if out.dtype not in OUT_DTYPES:
+        raise TypeError("out must be torch.bfloat16 or torch.float32")
+    return out, out.dtype == torch.float32
 
 
 def packed_bytes_w8(N, K):
@@ -633,10 +658,9 @@ def packed_bytes_w8(N, K):
 
 
 def _bytes_w8(N, K):
-    nb = packed_bytes_w8(N, K)
-    if nb == 0 and N != 0:
-        _check(W4_ERR_SHAPE, "w4_w8_packed_bytes")
-    return nb
+    if N >= 0 and 0 < K <= 130944 and K % GROUP == 0:
+        return (N + 15) // 16 * 16 * K
+    _check(W4_ERR_SHAPE, "w4_w8_packed_bytes")
 
 
 def quantize_w8(W, out=None):
@@ -645,53 +669,48 @@ def quantize_w8(W, out=None):
     [E, N, K] gives codes [E, packed_bytes_w8(N, K)] and scales [E, N]."""
     if not isinstance(W, torch.Tensor) or W.dim() not in (2, 3):
         raise TypeError("W must be a 2-D (or, for experts, 3-D) torch.Tensor")
-    lead, (N, K) = tuple(W.shape[:-2]), W.shape[-2:]
-    _dev(W, torch.float32, "W")
+    dev, shape = _first(W, (torch.float32,), "W")
+    lead, (N, K) = shape[:-2], shape[-2:]
     nb = _bytes_w8(N, K)
     if out is None:
         out = (torch.empty(lead + (nb,), dtype=torch.int8, device=W.device),
                torch.empty(lead + (N,), dtype=torch.float32, device=W.device))
     q, d = out
-    _one_device([W, q, d], "quantize_w8")
-    _sized(q, torch.int8, lead + (nb,), "q"), _sized(d, torch.float32, lead + (N,), "d")
-    for w_, q_, d_ in (zip(W, q, d) if lead else ((W, q, d),)):
-        _launch("w4_quantize_w8", W.device, ctypes.c_void_p(w_.data_ptr()), N, K, ctypes.c_void_p(q_.data_ptr()),
-                ctypes.c_void_p(d_.data_ptr()))
+    pq, pd, pw = _ptr(q, torch.int8, dev, "q", lead + (nb,)), _ptr(d, torch.float32, dev, "d", lead + (N,)), W.data_ptr()
+    for e in range(lead[0] if lead else 1):
+        _launch("w4_quantize_w8", dev, pw + 4 * e * N * K, N, K, pq + e * nb, pd + 4 * e * N)
     return q, d
 
 
 def pack_w8(q_canon, out=None):
     """Codes int8 [N, K] (computed elsewhere) -> native layout int8 [packed_bytes_w8(N, K)]."""
-    N, K = _matrix(q_canon, "q_canon")
+    dev, N, K = _rows(q_canon, (torch.int8,), "q_canon")
     nb = _bytes_w8(N, K)
     q = out if out is not None else torch.empty(nb, dtype=torch.int8, device=q_canon.device)
-    _one_device([q_canon, q], "pack_w8")
-    _launch("w4_pack_w8", q_canon.device, _dev(q_canon, torch.int8, "q_canon"), N, K, _elements(q, torch.int8, nb, "q"))
+    _launch("w4_pack_w8", dev, q_canon.data_ptr(), N, K, _ptr(q, torch.int8, dev, "q", count=nb))
     return q
 
 
 def unpack_w8(q, N, K):
     """Native 8-bit codes -> int8 [N, K]."""
-    p = _elements(q, torch.int8, _bytes_w8(N, K), "q")
+    dev, _ = _first(q, (torch.int8,), "q")
+    p = _ptr(q, torch.int8, dev, "q", count=_bytes_w8(N, K))
     qc = torch.empty((N, K), dtype=torch.int8, device=q.device)
-    _launch("w4_unpack_w8", q.device, p, N, K, _dev(qc, torch.int8, "q_canon"))
+    _launch("w4_unpack_w8", dev, p, N, K, qc.data_ptr())
     return qc
 
 
 def quantize_tokens(x, out=None):
     """Activations [M, K] (bf16, or fp32) -> (xq int8 [M, K], sx fp32 [M]): one scale per token,
     codes in [-127, 127].  A token that holds a NaN or an infinity gets scale NaN and codes 0."""
-    M, K = _matrix(x, "x")
-    if x.dtype not in OUT_DTYPES:
-        raise TypeError(f"x must be torch.bfloat16 or torch.float32 (got {x.dtype})")
-    px = _dev(x, x.dtype, "x")
+    dev, M, K = _rows(x, OUT_DTYPES, "x")
     if out is None:
-        out = (torch.empty((M, K), dtype=torch.int8, device=x.device),
-               torch.empty(M, dtype=torch.float32, device=x.device))
-    xq, sx = out
-    _one_device([x, xq, sx], "quantize_tokens")
-    _launch("w4_quantize_tokens_f32" if x.dtype == torch.float32 else "w4_quantize_tokens", x.device, px, M, K,
-            _sized(xq, torch.int8, (M, K), "xq"), _sized(sx, torch.float32, (M,), "sx"))
+        xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        sx = torch.empty(M, dtype=torch.float32, device=x.device)
+    else:
+        xq, sx = out
+    _launch("w4_quantize_tokens_f32" if x.dtype == torch.float32 else "w4_quantize_tokens", dev, x.data_ptr(), M, K,
+            _ptr(xq, torch.int8, dev, "xq", (M, K)), _ptr(sx, torch.float32, dev, "sx", (M,)))
     return xq, sx
 
 
@@ -699,36 +718,40 @@ def linear_w8a8(xq, sx, q, d, N, out=None, out_dtype=torch.bfloat16):
     """y [M, N] = (sx x d) * (xq q^T): int8 tokens xq [M, K] with scales sx [M] times native 8-bit
     weights q with channel scales d [N], summed exactly.  y is bf16, or fp32 with
     out_dtype=torch.float32 (or an fp32 `out`)."""
-    M, K = _matrix(xq, "xq")
-    p = _dev(xq, torch.int8, "xq")
+    dev, M, K = _rows(xq, (torch.int8,), "xq")
     y, f32 = _output(out, out_dtype, M, N, xq.device)
-    _one_device([xq, sx, q, d, y], "linear_w8a8")
-    _launch("w4_linear_w8a8_f32" if f32 else "w4_linear_w8a8", xq.device, p, _sized(sx, torch.float32, (M,), "sx"), M, K,
-            _elements(q, torch.int8, _bytes_w8(N, K), "q"), _sized(d, torch.float32, (N,), "d"), N,
-            _sized(y, y.dtype, (M, N), "out"))
+    _launch("w4_linear_w8a8_f32" if f32 else "w4_linear_w8a8", dev, xq.data_ptr(),
+            _ptr(sx, torch.float32, dev, "sx", (M,)), M, K, _ptr(q, torch.int8, dev, "q", count=_bytes_w8(N, K)),
+            _ptr(d, torch.float32, dev, "d", (N,)), N, _ptr(y, y.dtype, dev, "out", (M, N)))
     return y
 
 
 def _experts(offsets):
-    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() < 1:
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 1:
         raise TypeError("offsets must be a 1-D torch.Tensor of experts + 1 values")
-    return offsets.numel() - 1
+    return offsets.shape[0] - 1
 
 
 def grouped_linear_w8a8(xq, sx, offsets, q, d, N, out=None, out_dtype=torch.bfloat16):
     """linear_w8a8 with rows sorted by expert: rows offsets[e] .. offsets[e + 1] - 1 of xq use
     expert e's weight (q [E, packed_bytes_w8(N, K)], d [E, N]; offsets int32 [E + 1] on the GPU).
     Rows of y that no expert owns are left as they were (undefined without `out`)."""
-    M, K = _matrix(xq, "xq")
     E = _experts(offsets)
-    p = _dev(xq, torch.int8, "xq")
+    dev, M, K = _rows(xq, (torch.int8,), "xq")
     y, f32 = _output(out, out_dtype, M, N, xq.device)
-    _one_device([xq, sx, offsets, q, d, y], "grouped_linear_w8a8")
-    _launch("w4_linear_grouped_w8a8_f32" if f32 else "w4_linear_grouped_w8a8", xq.device, p,
-            _sized(sx, torch.float32, (M,), "sx"), M, K, _dev(offsets, torch.int32, "offsets"), E,
-            _elements(q, torch.int8, E * _bytes_w8(N, K), "q"), _sized(d, torch.float32, (E, N), "d"), N,
-            _sized(y, y.dtype, (M, N), "out"))
+    _launch("w4_linear_grouped_w8a8_f32" if f32 else "w4_linear_grouped_w8a8", dev, xq.data_ptr(),
+            _ptr(sx, torch.float32, dev, "sx", (M,)), M, K, _ptr(offsets, torch.int32, dev, "offsets"), E,
+            _ptr(q, torch.int8, dev, "q", count=E * _bytes_w8(N, K)), _ptr(d, torch.float32, dev, "d", (E, N)), N,
+            _ptr(y, y.dtype, dev, "out", (M, N)))
     return y
+
+
+def _packed_sizes(N, K):
+    """(packed_bytes, scale_count) of a 4-bit matrix."""
+    if N >= 0 and 0 < K <= 1 << 24 and K % GROUP == 0:
+        rows, inputs = (N + 15) // 16 * 16, (K + 511) // 512 * 512
+        return rows * inputs // 2, rows * inputs // GROUP
+    _check(W4_ERR_SHAPE, "packed buffers")
 
 
 def quantize_rtn_experts(W, scale_dtype=torch.float32):
@@ -736,19 +759,16 @@ def quantize_rtn_experts(W, scale_dtype=torch.float32):
     scales [E, scale_count]), as grouped_linear takes them."""
     if not isinstance(W, torch.Tensor) or W.dim() != 3:
         raise TypeError("W must be a 3-D torch.Tensor")
+    dev, (E, N, K) = _first(W, (torch.float32,), "W")
     if scale_dtype not in SCALE_DTYPES:
         raise TypeError("scale_dtype must be torch.float32 or torch.bfloat16")
-    _dev(W, torch.float32, "W")
-    E, N, K = W.shape
-    nb, ns = packed_bytes(N, K), scale_count(N, K)
-    if nb == 0 and N != 0:
-        _check(W4_ERR_SHAPE, "packed buffers")
+    nb, ns = _packed_sizes(N, K)
     q = torch.empty((E, nb), dtype=torch.uint8, device=W.device)
     d = torch.empty((E, ns), dtype=scale_dtype, device=W.device)
     name = "w4_quantize_rtn_s16" if scale_dtype == torch.bfloat16 else "w4_quantize_rtn"
-    for w_, q_, d_ in zip(W, q, d):
-        _launch(name, W.device, ctypes.c_void_p(w_.data_ptr()), N, K, ctypes.c_void_p(q_.data_ptr()),
-                ctypes.c_void_p(d_.data_ptr()))
+    for e in range(E):
+        _launch(name, dev, W.data_ptr() + 4 * e * N * K, N, K, q.data_ptr() + e * nb,
+                d.data_ptr() + e * ns * d.element_size())
     return q, d
 
 
@@ -758,18 +778,15 @@ def grouped_linear(x, offsets, q, d, N, out=None, out_dtype=torch.bfloat16):
     [E, scale_count(N, K)], as quantize_rtn_experts gives them; offsets int32 [E + 1] on the GPU).
     y [M, N] is bf16, or fp32 with out_dtype=torch.float32 (or an fp32 `out`).  Rows of y that no
     expert owns are left as they were (undefined without `out`)."""
-    M, K = _matrix(x, "x")
     E = _experts(offsets)
-    p = _dev(x, torch.bfloat16, "x")
+    dev, M, K = _rows(x, (torch.bfloat16,), "x")
     sd = _scale_dtype(d)
-    nb, ns = packed_bytes(N, K), scale_count(N, K)
-    if nb == 0 and N != 0:
-        _check(W4_ERR_SHAPE, "packed buffers")
+    nb, ns = _packed_sizes(N, K)
     y, f32 = _output(out, out_dtype, M, N, x.device)
-    _one_device([x, offsets, q, d, y], "grouped_linear")
     name = "w4_linear_grouped" + ("_f32" if f32 else "") + ("_s16" if sd == torch.bfloat16 else "")
-    _launch(name, x.device, p, M, K, _dev(offsets, torch.int32, "offsets"), E, _elements(q, torch.uint8, E * nb, "q"),
-            _elements(d, sd, E * ns, "d"), N, _sized(y, y.dtype, (M, N), "out"))
+    _launch(name, dev, x.data_ptr(), M, K, _ptr(offsets, torch.int32, dev, "offsets"), E,
+            _ptr(q, torch.uint8, dev, "q", count=E * nb), _ptr(d, sd, dev, "d", count=E * ns), N,
+            _ptr(y, y.dtype, dev, "out", (M, N)))
     return y
 
 

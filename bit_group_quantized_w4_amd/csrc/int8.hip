@@ -16,8 +16,6 @@
 #include "w4_launch.h"
 #include "w4_rows.h"
 
-#include <float.h>
-
 
 namespace w4 {
 namespace {
@@ -32,59 +30,146 @@ __device__ __forceinline__ i32x4 mfma16x16x64(const i32x4& a, const i32x4& b, co
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ float load_f32(const float* p) { return *p; }
-__device__ __forceinline__ float load_f32(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
-
-// Code of v against the scale d: round half away of the IEEE quotient.
-__device__ __forceinline__ int code_of(float v, float d) {
-  const float t = v / d;
-  float r = truncf(t);
-  r = fabsf(t - r) >= 0.5f ? r + copysignf(1.0f, t) : r;
-  return (int)fminf(fmaxf(r, -kMaxCode8), kMaxCode8);
-}
-
 // Byte offset of input k of row n in the native layout.
 __device__ __forceinline__ int64_t native_at(int64_t n, int64_t k, int64_t K) {
   return ((n >> 4) * (K / kStep) + k / kStep) * 1024 + ((k >> 4) & 3) * 256 + (n & 15) * 16 + (k & 15);
 }
 
-// One block per row: the row's largest magnitude, then its codes.
-// kNative: rows are a weight's, written as tiles (rows N .. of the last row
-// block as zeros); otherwise tokens, written row-major.
-template <typename T, bool kNative>
-__global__ __launch_bounds__(256) void quantize_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t K,
-                                                            int8_t* __restrict__ q, float* __restrict__ scale) {
-  const int64_t row = blockIdx.x;
-  __shared__ float smax[4];
-  __shared__ int sbad[4];
-  float amax = 0.0f;
-  int bad = 0;
-  if (row < rows) {
-    for (int64_t k = threadIdx.x; k < K; k += 256) {
-      const float a = fabsf(load_f32(x + row * K + k));
-      bad |= !(a <= FLT_MAX);
-      amax = fmaxf(amax, a);
+// Code of v against the scale d: round half away of the IEEE quotient.
+__device__ __forceinline__ uint32_t code_of(float v, float d) {
+  const float t = v / d;
+  float r = truncf(t);
+  r = fabsf(t - r) >= 0.5f ? r + copysignf(1.0f, t) : r;
+  return (uint32_t)(int)fminf(fmaxf(r, -kMaxCode8), kMaxCode8) & 0xFFu;
+}
+
+// Value j of a 16-byte chunk: four fp32, or eight bf16.
+template <bool kF32>
+__device__ __forceinline__ float value_of(const uint4& c, int j) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  if constexpr (kF32) return __uint_as_float(w[j]);
+  return __uint_as_float(j & 1 ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+}
+
+// The largest magnitude bits of a chunk joined with `m`: as integers, a NaN is above
+// infinity and infinity above every finite value.  bf16: two maxima, one per half.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+template <bool kF32>
+__device__ __forceinline__ uint32_t max_bits(const uint4& c, uint32_t m) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kF32)
+      m = max(m, w[i] & 0x7FFFFFFFu);
+    else
+      m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m),
+                                                                 __builtin_bit_cast(u16x2, w[i] & 0x7FFF7FFFu)));
+  }
+  return m;
+}
+
+// Quantizes one row with `TPR` threads: the row's largest magnitude, then its codes.
+// The first C chunks of 16 bytes per thread stay in registers between the two, so
+// that a row is read once; what is left of a longer one is read again (from a cache).
+// kNative: rows of a weight, written as tiles; blocks go to the eight XCDs in turn,
+// and each XCD is given whole row blocks, row after row, so that the 16 bytes that
+// a row adds to each 256 meet in one L2.  Otherwise tokens, written row-major.
+//
+// Codes: with y = 1 / d rounded, v * y + 1.5 * 2^23 has the nearest integer of v * y in
+// its low bits, in one fma.  v * y is within 127.5 * 2^-24 of v / d, and the IEEE quotient
+// that the code is defined by within 2^-18 of it: together less than 2^-16, so the
+// code is the same unless v * y lies that near to a half-integer.  Where a thread
+// of the wavefront finds one of its chunk's values within 2^-15 of a half (3% of chunks
+// of normal weights), or the scale lies outside [2^-100, 2^100], the chunk's codes are
+// formed from the IEEE quotients.
+//
+// Bound by memory: 28672 x 8192 weights (1.17 GB) take 236 us (5.0 TB/s; a copy
+// reaches 4.9), 4099 x 28672 bf16 tokens (353 MB) 62 us (5.7 TB/s).
+template <bool kF32, bool kNative, int TPR, int C>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void quantize_rows_kernel(const void* __restrict__ x, int rows,
+                                                                              int padded, int K,
+                                                                              int8_t* __restrict__ q,
+                                                                              float* __restrict__ scale) {
+  constexpr int E = kF32 ? 4 : 8;                 // values per chunk
+  constexpr int RPB = TPR > 256 ? 1 : 256 / TPR;  // rows per block
+  const int at = threadIdx.x % TPR;
+  int row = blockIdx.x * RPB + (RPB > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0);
+  if constexpr (kNative) {
+    constexpr int kBlocks = kTileRows / RPB;  // blocks per row block
+    const int i = blockIdx.x / kXcds;
+    row = ((i / kBlocks) * kXcds + blockIdx.x % kXcds) * kTileRows + (i % kBlocks) * RPB +
+          (RPB > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0);
+  }
+  const bool real = row < rows;
+  // (a row of padding reads zeros, and so does a chunk past the row's end)
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(static_cast<const uint8_t*>(x) + (int64_t)(real ? row : 0) * K * (kF32 ? 4 : 2),
+                                              real ? (uint32_t)K * (kF32 ? 4u : 2u) : 0u);
+  const int chunks = K / E;
+  uint4 c[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) c[i] = bload<kNonTemporal>(rs, (uint32_t)(at + i * TPR) * 16u);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < C; ++i) m = max_bits<kF32>(c[i], m);
+  for (int i = at + C * TPR; i < chunks; i += TPR) m = max_bits<kF32>(bload<0>(rs, (uint32_t)i * 16u), m);
+  if constexpr (!kF32) m = max(m & 0xFFFFu, m >> 16) << 16;
+#pragma unroll
+  for (int s = 32; s; s >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, s));
+  if constexpr (TPR > 64) {
+    __shared__ uint32_t part[TPR / 64];
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < TPR / 64; ++w) m = max(m, part[w]);
+  }
+  const bool bad = m >= 0x7F800000u;
+  const float d = bad ? __uint_as_float(kNanBits) : __uint_as_float(m) / kMaxCode8;
+  const bool usable = !bad && d != 0.0f;
+  const float y = 1.0f / (usable ? d : 1.0f);
+  const bool far = !(d >= 0x1p-100f && d <= 0x1p+100f);
+  auto codes = [&](const uint4& v, uint32_t (&out)[E / 4]) {
+    constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
+    uint32_t b[E];
+    float worst = 0.0f;
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const float f = value_of<kF32>(v, j), r = fmaf(f, y, kMagic);
+      b[j] = __float_as_uint(r);
+      worst = fmaxf(worst, fabsf(fmaf(f, y, kMagic - r)));
+    }
+    if (__ballot(worst > 0.5f - 0x1p-15f || far)) {
+#pragma unroll
+      for (int j = 0; j < E; ++j) b[j] = usable ? code_of(value_of<kF32>(v, j), d) : 0;
+    }
+#pragma unroll
+    for (int w = 0; w < E / 4; ++w) {  // the low bytes of four words
+      const uint32_t lo = __builtin_amdgcn_perm(b[4 * w + 1], b[4 * w], 0x0C0C0400u);
+      const uint32_t hi = __builtin_amdgcn_perm(b[4 * w + 3], b[4 * w + 2], 0x04000C0Cu);
+      out[w] = lo | hi;
+    }
+  };
+  auto store = [&](int i, const uint32_t (&o)[E / 4]) {
+    int8_t* to = q + (kNative ? native_at(row, (int64_t)i * E, K) : (int64_t)row * K + (int64_t)i * E);
+    if constexpr (E == 8)
+      *reinterpret_cast<uint2*>(to) = make_uint2(o[0], o[1]);
+    else
+      *reinterpret_cast<uint32_t*>(to) = o[0];
+  };
+  if (row >= padded) return;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    if (at + i * TPR < chunks) {
+      uint32_t o[E / 4];
+      codes(c[i], o);
+      store(at + i * TPR, o);
     }
   }
-#pragma unroll
-  for (int s = 32; s; s >>= 1) {
-    amax = fmaxf(amax, __shfl_xor(amax, s));
-    bad |= __shfl_xor(bad, s);
+  for (int i = at + C * TPR; i < chunks; i += TPR) {
+    uint32_t o[E / 4];
+    codes(bload<0>(rs, (uint32_t)i * 16u), o);
+    store(i, o);
   }
-  if ((threadIdx.x & 63) == 0) {
-    smax[threadIdx.x >> 6] = amax;
-    sbad[threadIdx.x >> 6] = bad;
-  }
-  __syncthreads();
-  amax = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
-  bad = sbad[0] | sbad[1] | sbad[2] | sbad[3];
-  const float d = bad ? __uint_as_float(kNanBits) : amax / kMaxCode8;
-  const bool usable = !bad && d != 0.0f && row < rows;
-  for (int64_t k = threadIdx.x; k < K; k += 256) {
-    const int c = usable ? code_of(load_f32(x + row * K + k), d) : 0;
-    q[kNative ? native_at(row, k, K) : row * K + k] = (int8_t)c;
-  }
-  if (threadIdx.x == 0 && row < rows) scale[row] = d;
+  if (at == 0 && real) scale[row] = d;
 }
 
 // Canonical [N][K] <-> native tiles, 16 codes per thread.
@@ -662,20 +747,42 @@ hipError_t launch_w8a8(const I8Args& a, W8a8 kind, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_quantize_w8(const float* W, int64_t N, int64_t K, int8_t* q, float* d, hipStream_t stream) {
-  const unsigned blocks = (unsigned)((N + kTileRows - 1) / kTileRows * kTileRows);
-  quantize_rows_kernel<float, true><<<blocks, 256, 0, stream>>>(W, N, K, q, d);
+namespace {
+
+// A wavefront per row while four chunks per lane hold it, else 256 threads with up to
+// 16 chunks each, else 1024.
+template <bool kF32, bool kNative>
+hipError_t launch_quantize_rows(const void* x, int64_t rows, int64_t K, int8_t* q, float* scale, hipStream_t st) {
+  const int64_t padded = kNative ? (rows + kTileRows - 1) / kTileRows * kTileRows : rows;
+  const int64_t chunks = K / (kF32 ? 4 : 8);
+  // native: whole row blocks for each XCD in turn
+  const int64_t all = kNative ? (padded / kTileRows + kXcds - 1) / kXcds * kXcds * kTileRows : rows;
+  if (all > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  const unsigned n = (unsigned)all;
+  const int r = (int)rows, p = (int)padded, k = (int)K;
+  if (chunks <= 4 * 64)
+    quantize_rows_kernel<kF32, kNative, 64, 4><<<(n + 3) / 4, 256, 0, st>>>(x, r, p, k, q, scale);
+  else if (chunks <= 4 * 256)
+    quantize_rows_kernel<kF32, kNative, 256, 4><<<n, 256, 0, st>>>(x, r, p, k, q, scale);
+  else if (chunks <= 8 * 256)
+    quantize_rows_kernel<kF32, kNative, 256, 8><<<n, 256, 0, st>>>(x, r, p, k, q, scale);
+  else if (chunks <= 16 * 256)
+    quantize_rows_kernel<kF32, kNative, 256, 16><<<n, 256, 0, st>>>(x, r, p, k, q, scale);
+  else
+    quantize_rows_kernel<kF32, kNative, 1024, 16><<<n, 1024, 0, st>>>(x, r, p, k, q, scale);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_w8(const float* W, int64_t N, int64_t K, int8_t* q, float* d, hipStream_t stream) {
+  return launch_quantize_rows<true, true>(W, N, K, q, d, stream);
 }
 
 hipError_t launch_quantize_tokens(const void* x, bool f32, int64_t M, int64_t K, int8_t* xq, float* sx,
                                   hipStream_t stream) {
-  if (f32)
-    quantize_rows_kernel<float, false><<<(unsigned)M, 256, 0, stream>>>(static_cast<const float*>(x), M, K, xq, sx);
-  else
-    quantize_rows_kernel<uint16_t, false><<<(unsigned)M, 256, 0, stream>>>(static_cast<const uint16_t*>(x), M, K, xq,
-                                                                           sx);
-  return hipGetLastError();
+  return f32 ? launch_quantize_rows<true, false>(x, M, K, xq, sx, stream)
+             : launch_quantize_rows<false, false>(x, M, K, xq, sx, stream);
 }
 
 hipError_t launch_pack_w8(const int8_t* src, int64_t N, int64_t K, int8_t* dst, bool pack, hipStream_t stream) {
