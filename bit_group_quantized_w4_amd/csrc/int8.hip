@@ -16,7 +16,6 @@
 #include "w4_launch.h"
 #include "w4_rows.h"
 
-
 namespace w4 {
 namespace {
 
@@ -745,10 +744,6 @@ hipError_t launch_w8a8(const I8Args& a, W8a8 kind, hipStream_t st) {
   return blocks ? hipGetLastError() : hipErrorInvalidConfiguration;
 }
 
-}  // namespace
-
-namespace {
-
 // A wavefront per row while four chunks per lane hold it, else 256 threads with up to
 // 16 chunks each, else 1024.
 template <bool kF32, bool kNative>
@@ -787,6 +782,7 @@ hipError_t launch_quantize_tokens(const void* x, bool f32, int64_t M, int64_t K,
 
 hipError_t launch_pack_w8(const int8_t* src, int64_t N, int64_t K, int8_t* dst, bool pack, hipStream_t stream) {
   const int64_t chunks = (N + kTileRows - 1) / kTileRows * K;  // 16 rows x K codes / 16
+  if (chunks > (int64_t)256 * 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   const unsigned blocks = (unsigned)((chunks + 255) / 256);
   if (pack)
     repack_kernel<true><<<blocks, 256, 0, stream>>>(src, N, K, chunks, dst);

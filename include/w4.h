@@ -669,8 +669,10 @@ w4_status w4_linear_w8a8_f32(const int8_t* xq, const float* sx, int64_t M, int64
  *                  codes at q_packed + e * (its packed bytes) and its scales
  *                  at d + e * (its scale count), every one N x K.
  * Rows of y outside every expert's range (before offsets[0] and from
- * offsets[experts] on) are left as they were.  A row's result does not depend
- * on which other rows and experts the call holds.
+ * offsets[experts] on) are left as they were.  A row's 8-bit result does not
+ * depend on which other rows and experts the call holds; a 4-bit one may differ
+ * in the last bits between calls of different sizes (the kernel is chosen by M,
+ * N and experts, and sums in another order).
  */
 #define W4_MAX_EXPERTS 4096
 

@@ -186,6 +186,46 @@ def test_linear_w8a8(w4, gpu, M, N, K, out_dtype):
     assert same_bits(w4.linear_w8a8(txq, tsx, tq, td, N, out_dtype=out_dtype), y)
 
 
+def _w8a8_exact(xq, sx, c, d):
+    """The definition in 64 bits, on the GPU: sums of products below 2^53 are exact there."""
+    return ((xq.double() @ c.double().T.contiguous()) * sx.double()[:, None] * d.double()[None, :]).cpu().numpy()
+
+
+# At these sizes every kernel that the choice by estimated cost can take is taken, with its steps
+# along K an odd number, an even one, fewer than the ring of buffers, and with ragged tiles.
+@pytest.mark.parametrize("M,N,K", [
+    (9, 5000, 1152), (16, 9216, 2560), (13, 6000, 11264), (5, 9216, 9216), (3, 4090, 128),
+    (17, 9216, 640), (25, 17408, 128), (40, 9216, 640), (33, 9200, 128), (64, 9216, 1408), (200, 2561, 896),
+    (65, 17400, 384), (130, 9216, 128), (300, 5000, 1152), (200, 9216, 1152), (1025, 2561, 128), (300, 9201, 640),
+    (400, 17408, 256), (1025, 5000, 640), (2049, 2561, 384), (2048, 9216, 128),
+    (1500, 9216, 384), (2900, 5003, 1152), (700, 17408, 128), (1111, 17405, 640)])
+def test_linear_w8a8_wide(w4, gpu, M, N, K):
+    _say(f"linear_w8a8 M={M} N={N} K={K}")
+    xq, sx, q, d = _w8a8_inputs(M + N + K, M, N, K)
+    txq, tsx, tc, td = _dev(gpu, xq, sx, q, d)
+    tq, ref = w4.pack_w8(tc), _w8a8_exact(txq, tsx, tc, td)
+    check_w8a8(w4.linear_w8a8(txq, tsx, tq, td, N), ref, "bf16")
+    check_w8a8(w4.linear_w8a8(txq, tsx, tq, td, N, out_dtype=F32), ref, "fp32")
+
+
+@pytest.mark.parametrize("M,N", [(3, 70), (40, 70), (40, 64), (300, 70), (300, 9216), (700, 17408)])
+def test_linear_w8a8_tiny_and_huge_outputs(w4, gpu, M, N):
+    """Scales are powers of two, so that the fp32 value is exact, subnormal outputs among them, and a
+    bf16 output is its nearest, ties to even; what is too large is infinite."""
+    _say(f"linear_w8a8 tiny and huge outputs M={M} N={N}")
+    xq, _, q, _ = _w8a8_inputs(11, M, N, 128)
+    xq[1:, 40:] = 0  # smaller sums, halves of a bf16 step among them
+    txq, tc = _dev(gpu, xq, q)
+    sums = txq.double() @ tc.double().T.contiguous()
+    for es, ed in ((-70, -70), (-60, -66), (0, 0), (52, 60), (60, 52)):
+        sx, d = torch.full((M,), 2.0 ** es, device=gpu), torch.full((N,), 2.0 ** ed, device=gpu)
+        y32 = (sums * 2.0 ** (es + ed)).cpu().float()
+        for out_dtype in (BF16, F32):
+            y = w4.linear_w8a8(txq, sx, w4.pack_w8(tc), d, N, out_dtype=out_dtype).cpu()
+            want = y32.to(out_dtype)
+            assert torch.equal(y, want), f"2^{es} 2^{ed} {out_dtype}: {int((y != want).sum())} of {y.numel()} differ"
+
+
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_linear_w8a8_largest_sums(w4, gpu, M):
     """K = 130944 of products 2^14: the int32 sum ends 2^21 below its limit, at either sign."""
@@ -235,6 +275,21 @@ def test_linear_w8a8_far_outputs(w4, gpu):
     rows = torch.tensor([0, 1, 131071, 261871, 262000, M - 2, M - 1], device=gpu)
     ref = oracle.w8a8_linear_ref(xq[rows].cpu().numpy(), sx[rows].cpu().numpy(), c.cpu().numpy(), d.cpu().numpy())
     check_w8a8(y[rows], ref, "far outputs")
+
+
+@pytest.mark.parametrize("M", [3, 40, 300])
+@pytest.mark.parametrize("es,ed", [(-60, -60), (48, 48), (-60, 48)])
+def test_linear_w8a8_range_of_scales(w4, gpu, M, es, ed):
+    """The ends of the range of scales in which every intermediate is a normal fp32."""
+    _say(f"linear_w8a8 scales 2^{es}, 2^{ed} M={M}")
+    xq, _, q, _ = _w8a8_inputs(7, M, 70, 256)
+    xq[0] = 0
+    xq[0, 0] = 1  # sums down to single products
+    sx, d = np.full(M, 2.0 ** es, np.float32), np.full(70, 2.0 ** ed, np.float32)
+    txq, tsx, tc, td = _dev(gpu, xq, sx, q, d)
+    for out_dtype in (BF16, F32):
+        y = w4.linear_w8a8(txq, tsx, w4.pack_w8(tc), td, 70, out_dtype=out_dtype)
+        check_w8a8(y, oracle.w8a8_linear_ref(xq, sx, q, d), "scales")
 
 
 # ----------------------------------------------------------------------------
@@ -316,7 +371,27 @@ def test_grouped_linear(w4, gpu, si, out_dtype, scale_dtype):
                      y[first:first + rows]), "not reproducible"
 
 
-@pytest.mark.parametrize("N,K,sizes", [(2048, 2560, [1, 0, 2, 1, 4]), (1000, 4224, [40, 8, 0, 33]), (600, 9216, [5, 130, 0, 21]),
+@pytest.mark.parametrize("N,K,sizes", [
+    (5000, 640, [40, 0, 150, 33, 60]), (2561, 384, [100, 90, 80, 0, 20, 95, 110, 200]), (2561, 128, [400, 0, 700, 300]),
+    (1000, 1152, [300] * 9 + [0, 2000]), (5003, 256, [3000, 0, 500, 1500]), (9216, 128, [2, 0, 1, 1]), (9216, 3840, [2, 3]),
+    (70, 256, [500] * 10)])
+def test_grouped_linear_w8a8_wide(w4, gpu, N, K, sizes):
+    _say(f"grouped_linear_w8a8 sizes={sizes} N={N} K={K}")
+    rng = np.random.default_rng(N + K)
+    off = _offsets(sizes)
+    xq, sx = _codes(rng, int(off[-1]), K), rng.uniform(1e-3, 0.1, int(off[-1])).astype(np.float32)
+    q, d = _int8_experts(N, len(sizes), N, K)
+    txq, tsx, tc, td, toff = _dev(gpu, xq, sx, q, d, off)
+    tq = torch.stack([w4.pack_w8(tc[e]) for e in range(len(sizes))])
+    for out_dtype in (BF16, F32):
+        y = w4.grouped_linear_w8a8(txq, tsx, toff, tq, td, N, out_dtype=out_dtype)
+        for e, (a, b) in enumerate(zip(off[:-1], off[1:])):
+            if a < b:
+                check_w8a8(y[a:b], _w8a8_exact(txq[a:b], tsx[a:b], tc[e], td[e]), f"expert {e}")
+
+
+@pytest.mark.parametrize("N,K,sizes", [(2048, 640, [1] * 19 + [0, 3]), (2050, 256, [3, 0] * 11 + [17, 8, 1] * 8),
+                                       (2048, 2560, [1, 0, 2, 1, 4]), (1000, 4224, [40, 8, 0, 33]), (600, 9216, [5, 130, 0, 21]),
                                        (256, 28672, [3, 16]), (1, 128, [1, 2]), (2304, 2688, [290, 0, 45])])
 def test_grouped_linear_larger(w4, gpu, N, K, sizes):
     _say(f"grouped_linear N={N} K={K} sizes={sizes}")
@@ -421,6 +496,53 @@ def test_grouped_far_experts(w4, gpu):
     ref, absdot = _w4_ref(W[torch.from_numpy(rows).to(gpu)].cpu().numpy(), _bits(x)[1:], F32)
     check_w4(y[1:][:, torch.from_numpy(rows).to(gpu)].contiguous(), ref, absdot, "last expert")
     assert bool((y[0] == 0).all())  # zero scales
+
+
+def test_grouped_far_outputs(w4, gpu):
+    """Outputs past element 2^31 of y, rows of the last tiles of three experts."""
+    _say("grouped, M=262140 N=8200 K=128")
+    M, N, K, E = 262140, 8200, 128, 3
+    W, q, d = _w4_experts(w4, gpu, 12, E, N, K, BF16)
+    q8, d8 = w4.quantize_w8(W)
+    g = torch.Generator(device=gpu)
+    g.manual_seed(12)
+    x = torch.randn((M, K), generator=g, device=gpu).to(BF16)
+    off = torch.tensor([0, 131071, 261000, M], dtype=torch.int32, device=gpu)
+    rows = np.array([0, 131070, 131071, 260999, 261000, 262101, M - 2, M - 1])
+    expert = np.searchsorted([131071, 261000, M], rows, side="right")
+    trows = torch.from_numpy(rows).to(gpu)
+    y = w4.grouped_linear(x, off, q, d, N)
+    for e in range(E):
+        mine = expert == e
+        ref, absdot = _w4_ref(W[e].cpu().numpy(), _bits(x[trows[torch.from_numpy(mine).to(gpu)]]), BF16)
+        check_w4(y[trows[torch.from_numpy(mine).to(gpu)]], ref, absdot, f"expert {e}")
+    del y
+    xq, sx = w4.quantize_tokens(x)
+    y = w4.grouped_linear_w8a8(xq, sx, off, q8, d8, N)
+    for r, e in zip(rows.tolist(), expert.tolist()):
+        assert same_bits(w4.linear_w8a8(xq[r:r + 1].clone(), sx[r:r + 1].clone(), q8[e], d8[e].clone(), N), y[r:r + 1])
+
+
+def test_grouped_many_experts(w4, gpu):
+    """As many experts as a call takes, most without rows."""
+    _say("grouped, 4096 experts")
+    E, N, K = 4096, 16, 128
+    W = torch.from_numpy(np.random.default_rng(13).standard_normal((E, N, K)).astype(np.float32)).to(gpu)
+    q8, d8 = w4.quantize_w8(W)
+    q, d = w4.quantize_rtn_experts(W)
+    sizes = np.zeros(E, np.int64)
+    for e, s in ((0, 3), (63, 1), (64, 20), (1000, 40), (4031, 2), (4032, 1), (4095, 17)):
+        sizes[e] = s
+    off = _offsets(sizes)
+    x = workloads.random_activations(int(off[-1]), K, seed=13, device=gpu)
+    xq, sx = w4.quantize_tokens(x)
+    toff = torch.from_numpy(off).to(gpu)
+    y8, y4 = w4.grouped_linear_w8a8(xq, sx, toff, q8, d8, N), w4.grouped_linear(x, toff, q, d, N)
+    for e in np.flatnonzero(sizes):
+        a, b = off[e], off[e + 1]
+        assert same_bits(y8[a:b], w4.linear_w8a8(xq[a:b].clone(), sx[a:b].clone(), q8[e], d8[e].clone(), N))
+        ref, absdot = _w4_ref(W[e].cpu().numpy(), _bits(x)[a:b], F32)
+        check_w4(y4[a:b], ref, absdot, f"expert {e}")
 
 
 # ----------------------------------------------------------------------------
