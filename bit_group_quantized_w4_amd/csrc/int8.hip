@@ -195,7 +195,6 @@ struct I8Args {
   const float* d;
   void* y;
   int M, K, N, experts;
-  int wide;  // every row of y starts at a multiple of 16 bytes
 };
 
 template <bool kF32>
@@ -208,48 +207,100 @@ __device__ __forceinline__ void store_scaled(const I8Args& a, int m, int n, int 
     static_cast<uint16_t*>(a.y)[i] = f32_to_bf16_rne(v);
 }
 
-// Sums of TM row tiles, sixteen consecutive outputs from n0 on of rows m0, m0 + 16 ..., scaled and stored.
-template <int TM, bool kF32>
-__device__ __forceinline__ void store_tile(const I8Args& a, const RowTile& rt, int m0, int n0, const i32x4 (&acc)[TM][4]) {
-  if (n0 >= a.N) return;
-  const int count = min(16, a.N - n0);
-  float d[16];
+// Outputs by way of LDS: sixteen rows of 64 outputs that a wavefront holds in the
+// matrix unit's order are written to a stage of its own, kStagePitch words a row, and
+// stored from there 16 bytes per lane, so that one store covers whole lines of y (4096 x 9216
+// fp32 outputs of K = 1152: 94 us, and 115 us with each lane's outputs stored from its
+// registers; bf16 64 us either way).  Stores go by 16 bytes whatever the
+// alignment of a row of y, which the hardware allows (N = 9217: bf16 78 us, 140 us one
+// output at a time; fp32 99 and 211 us).
+// (The pitch of 68 words spreads sixteen rows over the banks.)
+constexpr int kStagePitch = 68, kStageBytes = 16 * kStagePitch * 4;
+
+// Stores rows m0 .. m0 + 15 below m1, outputs n0 .. n0 + 63 below N: value(word, s, e) of the
+// staged words is the output of row m0 + stage_row(s) and column n0 + stage_col() + e.
+template <bool kF32>
+constexpr int kStageOut = kF32 ? 4 : 8;  // consecutive outputs per lane
+template <bool kF32>
+__device__ __forceinline__ int stage_col() {
+  return kStageOut<kF32> * ((threadIdx.x & 63) % (64 / kStageOut<kF32>));
+}
+template <bool kF32>
+__device__ __forceinline__ int stage_row(int s) {
+  return kStageOut<kF32> * s + (threadIdx.x & 63) / (64 / kStageOut<kF32>);
+}
+template <bool kF32, class Value>
+__device__ __forceinline__ void store_stage(const uint32_t* stage, void* y, int N, int m0, int m1, int n0, Value value) {
+  constexpr int E = kStageOut<kF32>;
+  // the stage is this wavefront's own, and its LDS operations run in order
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+  const int n = n0 + stage_col<kF32>(), count = min(E, N - n);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) d[e] = a.d[(int64_t)rt.expert * a.N + n0 + min(e, count - 1)];
+  for (int s = 0; s < 16 / E; ++s) {
+    const int m = m0 + stage_row<kF32>(s);
+    if (m >= m1 || count <= 0) continue;
+    const uint4* from = reinterpret_cast<const uint4*>(stage + stage_row<kF32>(s) * kStagePitch + stage_col<kF32>());
+    float v[E];
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int m = m0 + 16 * i;
-    if (m >= rt.r1) continue;
-    const float sx = a.sx[m];
-    float v[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = (float)acc[i][e >> 2][e & 3] * sx * d[e];
-    const int64_t at = (int64_t)m * a.N + n0;
+    for (int e = 0; e < E; e += 4) {
+      const uint4 w = from[e / 4];
+      v[e] = value(w.x, s, e);
+      v[e + 1] = value(w.y, s, e + 1);
+      v[e + 2] = value(w.z, s, e + 2);
+      v[e + 3] = value(w.w, s, e + 3);
+    }
+    const int64_t at = (int64_t)m * N + n;
     if constexpr (kF32) {
-      float* y = static_cast<float*>(a.y) + at;
-      if (a.wide && count == 16) {
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(y + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+      float* to = static_cast<float*>(y) + at;
+      if (count == E) {
+        __builtin_memcpy(to, v, 16);
       } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (e < count) y[e] = v[e];
+        for (int e = 0; e < E; ++e)
+          if (e < count) to[e] = v[e];
       }
     } else {
-      uint16_t* y = static_cast<uint16_t*>(a.y) + at;
-      if (a.wide && count == 16) {
-        uint32_t u[8];
+      uint16_t* to = static_cast<uint16_t*>(y) + at;
+      uint32_t u[E / 2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          u[e] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
-        *reinterpret_cast<uint4*>(y) = make_uint4(u[0], u[1], u[2], u[3]);
-        *reinterpret_cast<uint4*>(y + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+      for (int e = 0; e < E / 2; ++e) u[e] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
+      if (count == E) {
+        __builtin_memcpy(to, u, 16);
       } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (e < count) y[e] = f32_to_bf16_rne(v[e]);
+        for (int e = 0; e < E; ++e)
+          if (e < count) to[e] = (uint16_t)(u[e / 2] >> (16 * (e & 1)));
       }
     }
+  }
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Sums of TM row tiles of a wavefront, lane l's outputs n0 + 16 (l / 16) .. + 15 of rows
+// m0 + l % 16 + 16 i, scaled and stored by way of `stage` (kStageBytes of the
+// wavefront's own).
+template <int TM, bool kF32>
+__device__ __forceinline__ void store_tile(const I8Args& a, const RowTile& rt, int m0, int n0, const i32x4 (&acc)[TM][4],
+                                           uint8_t* stage) {
+  constexpr int E = kStageOut<kF32>;
+  uint32_t* words = reinterpret_cast<uint32_t*>(stage);
+  const int lane = threadIdx.x & 63;
+  float d[E], sx[TM][16 / E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) d[e] = a.d[(int64_t)rt.expert * a.N + min(n0 + stage_col<kF32>() + e, a.N - 1)];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int s = 0; s < 16 / E; ++s) sx[i][s] = a.sx[min(m0 + 16 * i + stage_row<kF32>(s), rt.r1 - 1)];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<i32x4*>(words + (lane & 15) * kStagePitch + 16 * (lane >> 4) + 4 * j) = acc[i][j];
+    store_stage<kF32>(words, a.y, a.N, m0 + 16 * i, rt.r1, n0,
+                      [&](uint32_t w, int s, int e) { return (float)(int)w * sx[i][s] * d[e]; });
   }
 }
 
@@ -365,7 +416,8 @@ __global__ __launch_bounds__(NW * 64) void w8a8_stream_kernel(const I8Args a) {
 // load holds up the wavefront for the 16 cycles that the address unit of the CU
 // takes for it, which eight wavefronts would otherwise spend in turn before any
 // product (4096 rows of 17408 x 5120: 361 us with all reads and loads first, 338
-// with both spread; 2161 TOP/s).  At that rate the power limit lowers the clock.
+// with both spread).  Now 313 to 329 us, 2.2 to 2.3 POP/s, by the clock that the power
+// limit leaves at that rate.
 //
 // Rows past the tile's last, row blocks past the matrix's last and steps past the
 // last one lie outside their buffers: such loads read no memory and give zeros.
@@ -494,9 +546,9 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void w8a8_tile_kernel(const I8Arg
     step(s + 1, lds1, lds0);
   }
   multiply(1, 1, [](int) {});
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load into LDS outlives the block
-
-  store_tile<TM, kF32>(a, rt, rt.r0 + 16 * wm * TM + nl, 16 * rb0 + 64 * wn + 16 * kb, acc);
+  all_done();  // no load into LDS is left, and nothing reads what the stages overwrite
+  static_assert(NW * kStageBytes <= kBuffer, "stages fit a buffer");
+  store_tile<TM, kF32>(a, rt, rt.r0 + 16 * wm * TM, 16 * rb0 + 64 * wn, acc, lds0 + wave * kStageBytes);
 }
 
 // The same for fewer rows, where a launch has too few tiles to fill the GPU and
@@ -507,8 +559,10 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void w8a8_tile_kernel(const I8Arg
 // 64 bytes of a row per step: lane l of a load takes row l / 4 of sixteen and its
 // chunk (l % 4) ^ t, t = 0, 2, 3, 1 for rows 0-3, 4-7, 8-11, 12-15, which keeps the
 // operand reads free of bank conflicts (LDS serves lanes 0-3, 12-15 and 20-27 of
-// a 16-byte read together).  333 rows of 2561 x 9216: 25.8 us with 64 x 64 tiles and
-// two groups, 52.2 us as 128 x 128 tiles of the kernel above, 30.6 us streamed.
+// a 16-byte read together).  333 rows of 2561 x 9216: 22.3 us with 64 x 64 tiles and
+// two groups, 43 us as 128 x 128 tiles of the kernel above.  Bound by what L2 delivers: a
+// block alone takes 0.12 us per 128 inputs, 246 of them at once 0.24 us (16 TB/s); four
+// groups, twice the loads in flight, take 1 us longer.
 __device__ __forceinline__ uint32_t quad_swizzle(int t) { return (0x78u >> (2 * t)) & 3u; }
 
 template <int WM, int WN, int TM, int G, bool kF32>
@@ -616,10 +670,10 @@ __global__ __launch_bounds__(WM* WN* G * 64) void w8a8_deep_kernel(const I8Args 
   }
   multiply(1, 1, [](int) {});
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0): no load into LDS outlives the loop
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0): no load into LDS is left,
+  __builtin_amdgcn_s_barrier();        // and nothing reads what is overwritten now
+  asm volatile("" ::: "memory");
   if constexpr (G > 1) {
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
     // chunk c of a group's sums, 1 KiB per wavefront, in buffer c % 4
     auto chunk = [&](int gg, int c) {
       uint8_t* b = c % 4 == 0 ? lds0 : c % 4 == 1 ? lds1 : c % 4 == 2 ? lds2 : lds3;
@@ -636,7 +690,10 @@ __global__ __launch_bounds__(WM* WN* G * 64) void w8a8_deep_kernel(const I8Args 
 #pragma unroll
       for (int c = 0; c < TM * TN; ++c) acc[c / TN][c % TN] += *chunk(gg, c);
   }
-  store_tile<TM, kF32>(a, rt, rt.r0 + 16 * wm * TM + nl, 16 * rb0 + 64 * wn + 16 * kb, acc);
+  // (the first group's part of the buffers holds no sums)
+  static_assert(NW <= 4 && kStageBytes <= kBuffer, "a stage per buffer");
+  uint8_t* stage = wave == 0 ? lds0 : wave == 1 ? lds1 : wave == 2 ? lds2 : lds3;
+  store_tile<TM, kF32>(a, rt, rt.r0 + 16 * wm * TM, 16 * rb0 + 64 * wn, acc, stage);
 }
 
 // ---------------------------------------------------------------------------
@@ -794,8 +851,7 @@ hipError_t launch_pack_w8(const int8_t* src, int64_t N, int64_t K, int8_t* dst, 
 hipError_t launch_linear_w8a8(const int8_t* xq, const float* sx, int64_t M, int64_t K, const int32_t* offsets,
                               int64_t experts, const int8_t* q, const float* d, int64_t N, void* y, bool f32,
                               hipStream_t stream) {
-  const I8Args a{xq, sx, offsets, q, d, y, (int)M, (int)K, (int)N, (int)experts,
-                 (reinterpret_cast<uintptr_t>(y) | (uintptr_t)(N * (f32 ? 4 : 2))) % 16 == 0};
+  const I8Args a{xq, sx, offsets, q, d, y, (int)M, (int)K, (int)N, (int)experts};
   return f32 ? launch_w8a8<true>(a, choose_w8a8(M, N, K, experts), stream)
              : launch_w8a8<false>(a, choose_w8a8(M, N, K, experts), stream);
 }
