@@ -48,9 +48,9 @@ __device__ __forceinline__ f32x4 mfma16x16x32(const bf16x8& a, const bf16x8& b, 
 // a group past its last reads zeros without touching memory, so that every load is
 // unconditional.  Codes are read through the caches, since an expert with more than
 // 16 rows is read by several blocks.  Bound by the latency of a few dependent loads
-// (offsets, then codes): two tokens of two experts of 64, 2048 x 2560 each, 10.9 us for
-// 44.7 MB (4.1 TB/s); three or four groups in flight, and past the caches, took 12.7
-// and 14.0 us.
+// (offsets, then codes): two tokens of two experts of 64, 2048 x 2560 each, 9.7 us for
+// 44.7 MB (4.6 TB/s) in a run of calls, 10.9 us as graph nodes; three or four groups in flight, and past the caches, took 12.7
+// and 14.0 us there.
 template <int R, int NW, bool S16, bool kF32>
 __global__ __launch_bounds__(NW * 64) void grouped_stream_kernel(const GroupedArgs a) {
   constexpr int D = 2;
@@ -171,7 +171,8 @@ __global__ __launch_bounds__(NW * 64) void grouped_stream_kernel(const GroupedAr
 // codes and the loads.  The barrier of a step stands before the last tile's products
 // of the group before: beside these the operands of the new group are read.
 //
-// 8190 rows of eight experts, 9216 x 2560: 398 us (972 TFLOP/s).  Bound by the issue of
+// 8190 rows of eight experts, 9216 x 2560: 390 us (990 TFLOP/s; up to 425 us where the
+// power limit lowers the clock).  Bound by the issue of
 // vector instructions: an MFMA takes about nine of its sixteen cycles to issue and
 // each vector instruction four more, of which there are 2.9 per MFMA (widening 1.75,
 // accumulation 1).  64 rows per block (two blocks of four wavefronts per CU, whose

@@ -82,8 +82,8 @@ __device__ __forceinline__ uint32_t max_bits(const uint4& c, uint32_t m) {
 // of normal weights), or the scale lies outside [2^-100, 2^100], the chunk's codes are
 // formed from the IEEE quotients.
 //
-// Bound by memory: 28672 x 8192 weights (1.17 GB) take 236 us (5.0 TB/s; a copy
-// reaches 4.9), 4099 x 28672 bf16 tokens (353 MB) 62 us (5.7 TB/s).
+// Bound by memory: 28672 x 8192 weights (1.17 GB) take 232 us (5.1 TB/s; a copy
+// reaches 4.9), 4099 x 28672 bf16 tokens (353 MB) 58.6 us (6.0 TB/s).
 template <bool kF32, bool kNative, int TPR, int C>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void quantize_rows_kernel(const void* __restrict__ x, int rows,
                                                                               int padded, int K,
@@ -309,7 +309,7 @@ __device__ __forceinline__ void store_tile(const I8Args& a, const RowTile& rt, i
 // A[l % 16][16 (l / 16) .. + 15] of x, the tile's B operand and
 // D[4 (l / 16) + j][l % 16], j = 0..3, all straight from memory.
 //
-// Bound by the weight stream: 13 rows of 28672 x 8192 take 41.5 us (5.7 TB/s).
+// Bound by the weight stream: 13 rows of 28672 x 8192 take 40 us (5.9 TB/s).
 // kStream reads the weights past the caches (47.6 us without).  Weights that may
 // still lie in the 256 MB last-level cache from their last use are read through
 // it: 2560 x 9216 at one row takes 6.6 us against 9.3 us.
