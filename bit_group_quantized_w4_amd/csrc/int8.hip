@@ -703,16 +703,19 @@ enum class W8a8 { kTile256, kTile128, kDeep128, kDeep64x128, kDeep64, kStream32x
 
 // The kernel for M rows shared out over `experts` matrices of N x K (their true
 // sizes are on the GPU: all are taken to be as busy as the average one).  Up to 16
-// rows each the weight stream is all there is to do.  Beyond that the smallest
+// rows each the weight stream is all there is to do; where an average of more than 12
+// means that many experts have more than 16, two row tiles per block read the weights of
+// those once (1024 rows of 64 experts of 1408 x 2560: 50.1 us against 58.6; 720 rows of 64 of
+// 2048 x 2048 49.8 and 50.9, but 88 rows of 8 of 2560 x 2560 13.5 and 11.9).  Beyond that the smallest
 // estimate wins, in us per 128 inputs, from times measured on the 2560 x 9216,
 // 9216 x 2560, 28672 x 8192 and 17408 x 5120 matrices at 32 to 4096 rows: `one` while
 // every block has a CU for itself, `all` for each further full set of `slots` blocks.
 // Small tiles win until the larger ones fill the GPU: 512 rows of 2560 x 9216 take
 // 27 us as 64 x 128 (160 blocks), 35 us as 64 x 64 and 48 us as 128 x 128 (80 blocks);
 // at 2048 rows 69, 82 and 60 us.
-W8a8 choose_w8a8(int64_t M, int64_t N, int64_t K, int64_t experts) {
+W8a8 choose_w8a8(int64_t M, int64_t N, int64_t experts, bool grouped) {
   const int64_t busy = experts < M ? experts : M, rows = (M + busy - 1) / busy;
-  if (rows <= 16) return W8a8::kRows16;
+  if (rows <= 16) return rows <= 12 || M <= 16 ? W8a8::kRows16 : W8a8::kStream32x64;
   struct Shape {
     W8a8 kind;
     int BM, BN, slots;
@@ -730,8 +733,10 @@ W8a8 choose_w8a8(int64_t M, int64_t N, int64_t K, int64_t experts) {
     const int64_t blocks = busy * ((rows + s.BM - 1) / s.BM) * ((N + s.BN - 1) / s.BN);
     double cost = s.one;
     if (blocks > 256) {
-      // the largest tiles run in whole rounds; smaller ones fill the gaps
-      const double rounds = s.slots == 256 && s.BM == 256 ? (double)((blocks + 255) / 256) : (double)blocks / s.slots;
+      // The largest tiles run in whole rounds; smaller ones fill the gaps, and so do the
+      // experts' partial tiles, which take less power (4096 rows of 16 experts of 5120 x 4096:
+      // 127 us as 256 x 256, 148 as 128 x 128; 2048 rows 114 and 96).
+      const double rounds = s.BM == 256 && !grouped ? (double)((blocks + 255) / 256) : (double)blocks / s.slots;
       cost = rounds * s.all > s.one ? rounds * s.all : s.one;
     }
     if (least == 0 || cost < least) {
@@ -852,8 +857,8 @@ hipError_t launch_linear_w8a8(const int8_t* xq, const float* sx, int64_t M, int6
                               int64_t experts, const int8_t* q, const float* d, int64_t N, void* y, bool f32,
                               hipStream_t stream) {
   const I8Args a{xq, sx, offsets, q, d, y, (int)M, (int)K, (int)N, (int)experts};
-  return f32 ? launch_w8a8<true>(a, choose_w8a8(M, N, K, experts), stream)
-             : launch_w8a8<false>(a, choose_w8a8(M, N, K, experts), stream);
+  const W8a8 kind = choose_w8a8(M, N, experts, offsets != nullptr);
+  return f32 ? launch_w8a8<true>(a, kind, stream) : launch_w8a8<false>(a, kind, stream);
 }
 
 }  // namespace w4

@@ -374,7 +374,7 @@ def test_grouped_linear(w4, gpu, si, out_dtype, scale_dtype):
 @pytest.mark.parametrize("N,K,sizes", [
     (5000, 640, [40, 0, 150, 33, 60]), (2561, 384, [100, 90, 80, 0, 20, 95, 110, 200]), (2561, 128, [400, 0, 700, 300]),
     (1000, 1152, [300] * 9 + [0, 2000]), (5003, 256, [3000, 0, 500, 1500]), (9216, 128, [2, 0, 1, 1]), (9216, 3840, [2, 3]),
-    (70, 256, [500] * 10)])
+    (70, 256, [500] * 10), (1037, 640, [40, 1, 0, 20, 3, 16, 17])])
 def test_grouped_linear_w8a8_wide(w4, gpu, N, K, sizes):
     _say(f"grouped_linear_w8a8 sizes={sizes} N={N} K={K}")
     rng = np.random.default_rng(N + K)
