@@ -559,7 +559,7 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void w8a8_tile_kernel(const I8Arg
 // 64 bytes of a row per step: lane l of a load takes row l / 4 of sixteen and its
 // chunk (l % 4) ^ t, t = 0, 2, 3, 1 for rows 0-3, 4-7, 8-11, 12-15, which keeps the
 // operand reads free of bank conflicts (LDS serves lanes 0-3, 12-15 and 20-27 of
-// a 16-byte read together).  333 rows of 2561 x 9216: 22.3 us with 64 x 64 tiles and
+// a 16-byte read together).  333 rows of 2561 x 9216: 21 us with 64 x 64 tiles and
 // two groups, 43 us as 128 x 128 tiles of the kernel above.  Bound by what L2 delivers: a
 // block alone takes 0.12 us per 128 inputs, 246 of them at once 0.24 us (16 TB/s); four
 // groups, twice the loads in flight, take 1 us longer.
