@@ -17,7 +17,14 @@
 namespace w4 {
 namespace {
 
-constexpr uint32_t kOob = 0x80000000u;  // buffer offsets from here on read zeros
+// Added to the offset of an operand of a group past the last one: one expert's codes, its
+// scales, and one tile's rows of x take less than 2 GiB each, so an offset inside its
+// buffer ends outside it and reads zeros without touching memory, and so does that of a row
+// of x that the tile does not have (below 2^28).  Only a row block past the expert's last
+// one, of codes within 128 MiB of 2 GiB, can end inside the buffer again (the sum wraps): it
+// reads codes of this expert, they meet zeros of x, and the outputs are past N, which no
+// kernel stores.
+constexpr uint32_t kOob = 0x80000000u;
 constexpr uint32_t kNeg15x2 = 0xBFC0BFC0u;  // bf16 -1.5 in both halves
 
 struct GroupedArgs {
@@ -45,11 +52,11 @@ __device__ __forceinline__ f32x4 mfma16x16x32(const bf16x8& a, const bf16x8& b, 
 // Streaming form, for experts with few rows: a block owns R row blocks of 16
 // outputs and a tile of 16 rows of x; its NW wavefronts divide the groups.  Each
 // wavefront keeps D groups of codes, scales and x in flight, straight from memory;
-// a group past its last reads zeros without touching memory, so that every load is
-// unconditional.  Codes are read through the caches, since an expert with more than
-// 16 rows is read by several blocks.  Bound by the latency of a few dependent loads
-// (offsets, then codes): two tokens of two experts of 64, 2048 x 2560 each, 9.7 us for
-// 44.7 MB (4.6 TB/s) in a run of calls, 10.9 us as graph nodes; three or four groups in flight, and past the caches, took 12.7
+// a group past its last reads zeros (see kOob), so that every load is unconditional.
+// Codes are read through the caches, since an expert with more than 16 rows is read by
+// several blocks.  Bound by the latency of a few dependent loads (offsets, then codes):
+// 16 rows of 64 experts of 2048 x 2560, 9.7 us for 44.7 MB (4.6 TB/s) in a run of calls,
+// 10.9 us as graph nodes; three or four groups in flight, and past the caches, took 12.7
 // and 14.0 us there.
 template <int R, int NW, bool S16, bool kF32>
 __global__ __launch_bounds__(NW * 64) void grouped_stream_kernel(const GroupedArgs a) {
@@ -178,8 +185,8 @@ __global__ __launch_bounds__(NW * 64) void grouped_stream_kernel(const GroupedAr
 // accumulation 1).  64 rows per block (two blocks of four wavefronts per CU, whose
 // barriers do not wait for each other) beat 128 rows in one block of eight (437 us).
 //
-// Steps past the last group (there are up to two, for the three buffers) read zeros
-// without touching memory.
+// Steps past the last group (there are up to two, for the three buffers) read zeros (see
+// kOob).
 template <int WM, int WN, int TM, bool S16, bool kF32>
 __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_tile_kernel(const GroupedArgs a, int panels) {
   constexpr int TN = 4, NW = WM * WN, BM = 16 * WM * TM, BN = 16 * WN * TN;

@@ -21,7 +21,13 @@ namespace {
 
 constexpr int kStep = 64;           // inputs per tile
 constexpr float kMaxCode8 = 127.0f;  // largest magnitude maps to code +-127
-constexpr uint32_t kOob = 0x80000000u;  // buffer offsets from here on read zeros
+// Added to the offset of an operand of a step past the last one: one matrix's codes, and
+// one tile's rows of x, take less than 2 GiB, so an offset inside its buffer ends outside
+// it and reads zeros without touching memory, and so does that of a row of x that the tile
+// does not have (at most 2^25).  Only a row block past the matrix's last one, of codes
+// within 32 MiB of 2 GiB, can end inside the buffer again (the sum wraps): it reads codes
+// of this matrix, they meet zeros of x, and the outputs are past N, which no kernel stores.
+constexpr uint32_t kOob = 0x80000000u;
 
 typedef int i32x4 __attribute__((__vector_size__(4 * sizeof(int))));
 
@@ -330,20 +336,20 @@ __global__ __launch_bounds__(NW * 64) void w8a8_stream_kernel(const I8Args a) {
       make_rsrc(a.q + (int64_t)rt.expert * nb * kTileRows * a.K, (uint32_t)nb * kTileRows * (uint32_t)a.K);
   const __amdgpu_buffer_rsrc_t rx =
       make_rsrc(a.xq + (int64_t)rt.r0 * a.K, (uint32_t)(rt.r1 - rt.r0) * (uint32_t)a.K);
+  // (row blocks past the matrix's last and rows past the tile's last lie outside the buffers)
   uint32_t wo[R], xo[MT];
 #pragma unroll
-  for (int r = 0; r < R; ++r) wo[r] = rb0 + r < nb ? ((uint32_t)(rb0 + r) * steps * 64u + lane) * 16u : kOob;
+  for (int r = 0; r < R; ++r) wo[r] = ((uint32_t)(rb0 + r) * steps * 64u + lane) * 16u;
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-    xo[i] = 16 * i + nl < rt.r1 - rt.r0 ? (uint32_t)(16 * i + nl) * (uint32_t)a.K + 16u * kb : kOob;
+  for (int i = 0; i < MT; ++i) xo[i] = (uint32_t)(16 * i + nl) * (uint32_t)a.K + 16u * kb;
 
   i32x4 acc[MT][R];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int r = 0; r < R; ++r) acc[i][r] = i32x4{0, 0, 0, 0};
-  // a ring of D steps' operands; a step past the wavefront's last reads zeros
-  // without touching memory, so that every load is unconditional
+  // a ring of D steps' operands; a step past the wavefront's last reads zeros (see
+  // kOob), so that every load is unconditional
   uint4 w[D][R], x[D][MT];
   auto issue = [&](int c, int s) {
     const uint32_t ow = s < s1 ? (uint32_t)s * 1024u : kOob, ox = s < s1 ? (uint32_t)s * kStep : kOob;
@@ -420,7 +426,7 @@ __global__ __launch_bounds__(NW * 64) void w8a8_stream_kernel(const I8Args a) {
 // limit leaves at that rate.
 //
 // Rows past the tile's last, row blocks past the matrix's last and steps past the
-// last one lie outside their buffers: such loads read no memory and give zeros.
+// last one lie outside their buffers: such loads give zeros (see kOob).
 constexpr int kRowBlockLds = 2 * 1024 + 64;
 
 template <int WM, int WN, int TM, int OCC, bool kF32>
