@@ -316,17 +316,12 @@ __device__ __forceinline__ void store_tile(const I8Args& a, const RowTile& rt, i
 // D[4 (l / 16) + j][l % 16], j = 0..3, all straight from memory.
 //
 // Bound by the weight stream: 13 rows of 28672 x 8192 take 40 us (5.9 TB/s).
-// kStream reads the weights past the caches (47.6 us without).  Weights that may
-// still lie in the 256 MB last-level cache from their last use are read through
-// it: 2560 x 9216 at one row takes 6.6 us against 9.3 us.
-template <int MT, int R, int NW, bool kStream, bool kF32>
-__global__ __launch_bounds__(NW * 64) void w8a8_stream_kernel(const I8Args a) {
+template <int MT, int R, int NW, int kCache, bool kF32>
+__device__ __forceinline__ void stream_row_tile(const I8Args& a, const RowTile& rt, int rb0,
+                                                i32x4 (&red)[NW][MT * R][64]) {
   constexpr int kWide = MT > R ? MT : R;
   constexpr int D = kWide >= 4 ? 2 : 8 / kWide;  // steps in flight: about 8 KiB per wavefront
-  const int nb = (a.N + kTileRows - 1) / kTileRows, panels = (nb + R - 1) / R;
-  const int t = blockIdx.x / panels, rb0 = (blockIdx.x - t * panels) * R;
-  RowTile rt;
-  if (!find_row_tile(a.offsets, a.experts, a.M, 16 * MT, t, rt)) return;
+  const int nb = (a.N + kTileRows - 1) / kTileRows;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nl = lane & 15, kb = lane >> 4;
   const int steps = a.K / kStep;
@@ -354,7 +349,7 @@ __global__ __launch_bounds__(NW * 64) void w8a8_stream_kernel(const I8Args a) {
   auto issue = [&](int c, int s) {
     const uint32_t ow = s < s1 ? (uint32_t)s * 1024u : kOob, ox = s < s1 ? (uint32_t)s * kStep : kOob;
 #pragma unroll
-    for (int r = 0; r < R; ++r) w[c][r] = bload<kStream ? kNonTemporal : 0>(rw, wo[r] + ow);
+    for (int r = 0; r < R; ++r) w[c][r] = bload<kCache>(rw, wo[r] + ow);
 #pragma unroll
     for (int i = 0; i < MT; ++i) x[c][i] = bload<0>(rx, xo[i] + ox);
   };
@@ -375,7 +370,6 @@ __global__ __launch_bounds__(NW * 64) void w8a8_stream_kernel(const I8Args a) {
     }
   }
 
-  __shared__ i32x4 red[NW][MT * R][64];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -395,6 +389,24 @@ __global__ __launch_bounds__(NW * 64) void w8a8_stream_kernel(const I8Args a) {
       if (m < rt.r1) store_scaled<kF32>(a, m, n, v[j], a.sx[m], d);
     }
   }
+}
+
+// kPast: an expert's weights are read past the caches, unless another row tile of the
+// expert reads them too.  (us as graph nodes, other weights than the last call's, through
+// the caches and past them: 13 rows of 28672 x 8192 44.8 and 39.5, 32 rows of 16 experts of
+// 5120 x 2560 37.0 and 32.4.  Where experts have several row tiles, past for all and for
+// the lone tiles only: 96 rows of 8 experts of 14336 x 4096, popularity falling as 1 / rank,
+// 92.6 and 86.1, all on one expert 51.3 and 39.6; 192 rows of 16 of 5120 x 2560, 44.6 and
+// 42.3, on one 24.1 and 18.7; evenly shared out equal.)
+template <int MT, int R, int NW, bool kPast, bool kF32>
+__global__ __launch_bounds__(NW * 64) void w8a8_stream_kernel(const I8Args a) {
+  const int nb = (a.N + kTileRows - 1) / kTileRows, panels = (nb + R - 1) / R;
+  const int t = blockIdx.x / panels, rb0 = (blockIdx.x - t * panels) * R;
+  RowTile rt;
+  if (!find_row_tile(a.offsets, a.experts, a.M, 16 * MT, t, rt)) return;
+  __shared__ i32x4 red[NW][MT * R][64];
+  if (kPast && rt.alone) stream_row_tile<MT, R, NW, kNonTemporal, kF32>(a, rt, rb0, red);
+  else stream_row_tile<MT, R, NW, 0, kF32>(a, rt, rb0, red);
 }
 
 // Tile form, for many rows: a block of WM x WN wavefronts owns BM = 16 WM TM rows
@@ -794,7 +806,13 @@ hipError_t launch_w8a8(const I8Args& a, W8a8 kind, hipStream_t st) {
       // and two; 9216 x 2560 6.6 and 6.4; 5120 x 17408 16.5 as two and four, 19.9 as
       // one and four).
       const int64_t nb = (a.N + kTileRows - 1) / kTileRows * (a.experts < a.M ? a.experts : a.M);
-      const bool past = (int64_t)a.experts * a.N * a.K >= (int64_t)64 << 20;  // larger than the caches keep
+      // Weights of 64 MiB or more are read past the caches, which is faster while each call has
+      // other weights than the last one (one row, us through the caches and past them: 17408 x 5120
+      // 20.4 and 18.2, 8192 x 8192 15.7 and 14.1).  Called again and again, a matrix that the
+      // 256 MB last-level cache holds is often faster through it (28672 x 8192 35.1 and 37.7; 17408
+      // x 5120 15.9 and 15.0, its 13 rows 17.8 and 18.3).  Below, the threshold leaves up to
+      // a tenth to the caches: 8192 x 5120 10.5 and 9.5, again and again 8.0 and 7.7.
+      const bool past = (int64_t)a.experts * a.N * a.K >= (int64_t)64 << 20;
       if (nb < 256) {
         if (grid(16, 16)) w8a8_stream_kernel<1, 1, 4, false, kF32><<<blocks, 256, 0, st>>>(a);
       } else if (nb < 512) {

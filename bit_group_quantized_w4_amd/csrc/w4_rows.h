@@ -13,6 +13,7 @@ namespace w4 {
 struct RowTile {
   int expert;
   int r0, r1;  // rows r0 .. r1-1, at most BM of them, at least one
+  bool alone;  // the expert has no other row tile
 };
 
 // Sum of v over this lane and the lanes before it, all 64 being active: prefix
@@ -40,6 +41,7 @@ __device__ __forceinline__ bool find_row_tile(const int* __restrict__ offsets, i
     o.expert = 0;
     o.r0 = t * BM;
     o.r1 = min(M, o.r0 + BM);
+    o.alone = M <= BM;
     return o.r0 < M;
   }
   const int lane = threadIdx.x & 63;
@@ -65,6 +67,7 @@ __device__ __forceinline__ bool find_row_tile(const int* __restrict__ offsets, i
       o.expert = e0 + l;
       o.r0 = __builtin_amdgcn_readlane(a, l) + (t - before - __builtin_amdgcn_readlane(s - n, l)) * BM;
       o.r1 = min(__builtin_amdgcn_readlane(b, l), o.r0 + BM);
+      o.alone = __builtin_amdgcn_readlane(n, l) == 1;
       return true;
     }
     before += __builtin_amdgcn_readlane(s, 63);
