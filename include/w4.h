@@ -25,10 +25,18 @@
  *   y[m][n]  = bf16_rne( sum_g d[n][g] * sum_{k in g} q[n][k] x[m][k] ),
  *            accumulated in fp32 per 128-group (the *_f32 entry points store
  *            the fp32 value itself, before rounding).
- *   Accuracy: the fp32 value v lies within 2e-3 * sum_k |w_hat[n][k] x[m][k]|
- *            + 1e-6 of the exact y; a bf16 output is the nearest-even bf16 of
+ *   Accuracy: the fp32 value v lies within
+ *              2e-3 * sum_k |w_hat[n][k] x[m][k]|
+ *              + 2^-10 * sum_k |d[n][k / 128] x[m][k]| + 1e-6
+ *            of the exact y; a bf16 output is the nearest-even bf16 of
  *            such a v, so it may differ from the exact y by that bound plus
  *            half a bf16 step (bf16 keeps 8 significant bits).
+ *            The middle term matters only where inputs that dominate a row
+ *            meet codes 0 (inputs with other codes add twice as much to the
+ *            first): the kernels form q x / 16 as (1.5 + q / 16) x - 1.5 x,
+ *            so an input of code 0 leaves the rounding of its own size.
+ *            2^-10 allows each of a group's 256 additions a whole step of
+ *            fp32; the most measured is 2^-17.
  *   Activations: a NaN or infinity anywhere in row m of x makes every
  *            y[m][n] NaN (the row is poisoned, as a non-finite weight group
  *            poisons its outputs).  The bound above is guaranteed while no

@@ -20,7 +20,8 @@ What it computes (sources are the public pages this project is built from):
   fp64.
 * ``admissible`` -- when an output counts as correct: within 2e-3 of
   sum |w_hat x| (plus 1e-6) of the exact value for fp32 outputs, and the
-  nearest-even bf16 of such a value for bf16 outputs.
+  nearest-even bf16 of such a value for bf16 outputs.  ``offset_scale_ref``
+  gives the sum that widens it where inputs that dominate a row meet codes 0.
 * ``pack_canonical`` / ``unpack_canonical`` -- the canonical two-codes-per-byte
   byte order used to compare codes bit for bit.
 * ``awq_search_ref`` and its steps -- activation-aware channel scaling before
@@ -46,16 +47,17 @@ from .awq import (ALPHAS, awq_output_error_ref, awq_search_ref, candidate_scales
 from .bf16 import bf16_bits_to_f64, f32_to_bf16_bits
 from .gptq import gptq_factor_ref, gptq_hessian_ref, gptq_quantize_ref, gptq_ref, output_error_ref
 from .int8 import QMAX8, W8A8_REL, pack_w8_ref, rtn_rows_ref, w8a8_linear_ref
-from .linear import dequantize_ref, w4_linear_ref
+from .linear import dequantize_ref, offset_scale_ref, w4_linear_ref
 from .packing import pack_canonical, unpack_canonical
 from .rtn import GROUP, NAN_BITS, QMAX, QMIN, rtn_quantize_ref
-from .tolerance import ABS_TOL, REL_TOL, admissible, rounding_interval, worst_ratio
+from .tolerance import ABS_TOL, OFFSET_TOL, REL_TOL, admissible, rounding_interval, worst_ratio
 
 __all__ = [
     "ABS_TOL",
     "ALPHAS",
     "GROUP",
     "NAN_BITS",
+    "OFFSET_TOL",
     "QMAX",
     "QMAX8",
     "QMIN",
@@ -75,6 +77,7 @@ __all__ = [
     "gptq_hessian_ref",
     "gptq_quantize_ref",
     "gptq_ref",
+    "offset_scale_ref",
     "output_error_ref",
     "pack_canonical",
     "pack_w8_ref",

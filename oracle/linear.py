@@ -36,6 +36,21 @@ def dequantize_ref(q, d):
     return np.repeat(d64, GROUP, axis=1) * q.astype(np.float64)
 
 
+def offset_scale_ref(x_bits, d):
+    """sum_k |d[n, k // 128] * x[m, k]| in float64, [M, N] (x_bits and d as for
+    w4_linear_ref; NaN where a row of x or a scale of d is not finite)."""
+    x = bf16_bits_to_f64(x_bits)
+    d = np.asarray(d)
+    d64 = bf16_bits_to_f64(d) if d.dtype == np.uint16 else d.astype(np.float64)
+    if x.ndim != 2 or x.shape[1] != d64.shape[1] * GROUP:
+        raise ValueError("x must be [M, K]")
+    finite = np.isfinite(x).all(axis=1)
+    sums = np.abs(np.where(finite[:, None], x, 0.0)).reshape(x.shape[0], -1, GROUP).sum(axis=2)
+    out = sums @ np.abs(d64).T
+    out[~finite, :] = np.nan
+    return out
+
+
 def w4_linear_ref(x_bits, q, d):
     """y[m, n] = sum_k x[m, k] * W_hat[n, k].
 

@@ -9,6 +9,13 @@ precision and no error bound; the bound this project holds the kernels to is
     |v - y_ref| <= REL * sum_k |w_hat[n,k] x[m,k]| + ABS,   REL = 2e-3, ABS = 1e-6,
 
 for the value v the kernel accumulates, with y_ref the exact (fp64) product.
+Where inputs that dominate a row meet codes 0, which the sum leaves out, the
+promise is wider by OFFSET * sum_k |d[n,k/128] x[m,k]|, OFFSET = 2^-10
+(``offset_scale_ref`` gives the sum; pass abs_ = ABS + OFFSET * sum).  Of a
+group with S = sum |x|, the start value -1.5 sum x takes 128 additions below
+1.5 S, and the products (1.5 + q/16) x another 128 below 2 S; each rounds by
+at most 2^-23 of that (a whole step), which is 448 * 2^-23 S, times 16 d:
+7168 * 2^-23 = 8.6e-4 of d S.
 Readings:
 
 * an fp32 output is that v itself, so it must satisfy the bound directly;
@@ -31,6 +38,7 @@ import numpy as np
 
 REL_TOL = 2e-3
 ABS_TOL = 1e-6
+OFFSET_TOL = 2.0 ** -10
 
 # (storage dtype, exponent-field shift, sign bit, bit pattern of +inf)
 _FORMATS = {

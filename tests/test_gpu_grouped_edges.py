@@ -42,3 +42,45 @@ def test_grouped_w8a8_few_rows_uneven(w4, gpu, N, K, sizes):
                 check_w8a8(y[a:b], _w8a8_exact(txq[a:b], tsx[a:b], tc[e], td[e]), f"expert {e}")
                 dense = w4.linear_w8a8(txq[a:b], tsx[a:b].clone(), tq[e], td[e].clone(), N, out_dtype=out_dtype)
                 assert same_bits(dense, y[a:b])
+
+
+# ----------------------------------------------------------------------------
+# 4-bit products: inputs that dominate a row
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("scale_dtype", [F32, BF16])
+@pytest.mark.parametrize("big", [1e3, 1e6, 1e8])
+@pytest.mark.parametrize("rows", [1, 4, 16, [5, 0, 3], [40, 20, 36], [200, 0, 150]])
+def test_dominant_inputs_at_zero_codes(w4, gpu, rows, big, scale_dtype):
+    """Inputs far above the rest of their row that meet codes 0 add nothing to sum |w_hat x|; what they
+    leave is within OFFSET_TOL of sum |d x|, in the dense kernels (a number of rows, each path) and in
+    the three grouped ones (the experts' rows)."""
+    _say(f"dominant inputs {big:g} rows={rows} scales {scale_dtype}")
+    N, K = 48, 640
+    sizes = rows if isinstance(rows, list) else [rows]
+    E, M, off = len(sizes), sum(sizes), _offsets(sizes)
+    rng = np.random.default_rng(M)
+    W = (rng.standard_normal((E, N, K)) * 0.02).astype(np.float32)
+    x = rng.standard_normal((M, K)).astype(np.float32)
+    for i, at in enumerate((5, 200, 383, 639)):
+        W[:, :, at] = 0.0
+        x[:, at] = big * (-1.0) ** i
+    xg = torch.from_numpy(x).to(gpu).to(BF16)
+    Wg = torch.from_numpy(W).to(gpu)
+    q, d = w4.quantize_rtn_experts(Wg, scale_dtype)
+    for out_dtype in (F32, BF16):
+        if E > 1:
+            ys = [w4.grouped_linear(xg, torch.from_numpy(off).to(gpu), q, d, N, out_dtype=out_dtype)]
+        else:
+            paths = ("gemv", "mfma", "auto") if M <= 4 else ("mfma", "auto")
+            ys = [w4.linear(xg, q[0], d[0], N, path=p, out_dtype=out_dtype) for p in paths]
+        for e, (a, b) in enumerate(zip(off[:-1], off[1:])):
+            if a == b:
+                continue
+            xb = _bits(xg)[a:b]
+            qc, dc = oracle.rtn_quantize_ref(W[e], "bf16" if scale_dtype == BF16 else "f32")
+            ref, absdot = oracle.w4_linear_ref(xb, qc, dc)
+            abs_ = oracle.ABS_TOL + oracle.OFFSET_TOL * oracle.offset_scale_ref(xb, dc)
+            for y in ys:
+                ok = oracle.admissible(_bits(y[a:b]), ref, absdot, "f32" if out_dtype == F32 else "bf16", abs_=abs_)
+                assert ok.all(), f"expert {e} {out_dtype}: {int((~ok).sum())} of {ok.size} outputs out of tolerance"
