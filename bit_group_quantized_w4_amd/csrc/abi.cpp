@@ -236,6 +236,7 @@ w4_status linear_w8a8(const int8_t* xq, const float* sx, int64_t M, int64_t K, b
   if (M == 0 || N == 0 || experts == 0) return W4_OK;
   const size_t qb = w4_w8_packed_bytes(N, K);
   if (qb >= (size_t)1 << 31) return W4_ERR_SHAPE;  // one matrix is addressed with 32-bit offsets
+  if (!w4::fits_linear_w8a8(M, N, experts, grouped)) return W4_ERR_SHAPE;
   if (!xq || !sx || !q || !d || !y || (grouped && !offsets)) return W4_ERR_NULL;
   if (!aligned(xq, 16) || !aligned(q, 16) || !aligned(sx, 4) || !aligned(d, 4) || !aligned(y, out) ||
       !aligned(offsets, 4))
@@ -257,6 +258,7 @@ w4_status linear_grouped(const uint16_t* x, int64_t M, int64_t K, const int32_t*
   if (M == 0 || N == 0 || experts == 0) return W4_OK;
   const size_t qb = w4_packed_bytes(N, K), db = (s16 ? 2 : 4) * w4_scale_count(N, K);
   if (qb >= (size_t)1 << 31) return W4_ERR_SHAPE;  // one matrix is addressed with 32-bit offsets
+  if (!w4::fits_linear_grouped(M, N, experts)) return W4_ERR_SHAPE;
   if (!x || !offsets || !q || !d || !y) return W4_ERR_NULL;
   if (!aligned(x, 16) || !aligned(offsets, 4) || !aligned(q, 16) || !aligned(d, 16) || !aligned(y, out))
     return W4_ERR_ALIGN;

@@ -420,23 +420,42 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void grouped_tile_kernel(const Grou
 // (256 rows of 16 experts of 5120 x 2560: 34.8 us, 38.0 streamed, 43.3 as 64 rows; 4096
 // rows of 64 of 1408 x 2560: 71.4 and 81.3); beyond, 64 rows (1024 rows of eight of
 // 9216 x 2560: 75.6 us, 86.0 as 32 rows).
+struct GroupedGrid {
+  int BM, threads;
+  bool four;
+  int64_t panels, blocks;
+};
+
+GroupedGrid grouped_grid(int64_t M, int64_t N, int64_t experts) {
+  const int64_t busy = experts < M ? experts : M, rows = (M + busy - 1) / busy;
+  const int64_t nb = (N + kTileRows - 1) / kTileRows;
+  GroupedGrid g;
+  g.four = busy * nb >= 2560;
+  g.BM = rows <= 8 ? 16 : rows <= 64 ? 32 : 64;
+  g.threads = rows > 8 ? 256 : 128;
+  const int BN = rows > 8 ? 256 : g.four ? 64 : 32;
+  g.panels = (N + BN - 1) / BN;
+  g.blocks = max_row_tiles(M, experts, true, g.BM) * g.panels;
+  return g;
+}
+
 template <bool S16, bool kF32>
 hipError_t launch_grouped(const GroupedArgs& a, hipStream_t st) {
-  const int64_t busy = a.experts < a.M ? a.experts : a.M, rows = (a.M + busy - 1) / busy;
-  const int64_t nb = (a.N + kTileRows - 1) / kTileRows;
-  const bool four = busy * nb >= 2560;
-  const int BM = rows <= 8 ? 16 : rows <= 64 ? 32 : 64, BN = rows > 8 ? 256 : four ? 64 : 32;
-  const int64_t panels = (a.N + BN - 1) / BN, blocks = max_row_tiles(a.M, a.experts, true, BM) * panels;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  const unsigned n = (unsigned)blocks;
-  if (rows > 64) grouped_tile_kernel<1, 4, 4, S16, kF32><<<n, 256, 0, st>>>(a, (int)panels);
-  else if (rows > 8) grouped_tile_kernel<1, 4, 2, S16, kF32><<<n, 256, 0, st>>>(a, (int)panels);
-  else if (four) grouped_stream_kernel<4, 2, S16, kF32><<<n, 128, 0, st>>>(a);
+  const GroupedGrid g = grouped_grid(a.M, a.N, a.experts);
+  const unsigned n = (unsigned)g.blocks;
+  if (g.BM == 64) grouped_tile_kernel<1, 4, 4, S16, kF32><<<n, 256, 0, st>>>(a, (int)g.panels);
+  else if (g.BM == 32) grouped_tile_kernel<1, 4, 2, S16, kF32><<<n, 256, 0, st>>>(a, (int)g.panels);
+  else if (g.four) grouped_stream_kernel<4, 2, S16, kF32><<<n, 128, 0, st>>>(a);
   else grouped_stream_kernel<2, 2, S16, kF32><<<n, 128, 0, st>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
+
+bool fits_linear_grouped(int64_t M, int64_t N, int64_t experts) {
+  const GroupedGrid g = grouped_grid(M, N, experts);
+  return g.blocks * g.threads < kMaxThreads;
+}
 
 hipError_t launch_linear_grouped(const uint16_t* x, int64_t M, int64_t K, const int32_t* offsets, int64_t experts,
                                  const uint8_t* q, const void* d, bool s16, int64_t N, void* y, bool f32,

@@ -765,47 +765,73 @@ W8a8 choose_w8a8(int64_t M, int64_t N, int64_t experts, bool grouped) {
   return best;
 }
 
-// Blocks of row tiles of BM rows times panels of BN outputs, or 0 if there are too many.
-unsigned block_count(const I8Args& a, int BM, int BN, int* panels) {
-  *panels = (a.N + BN - 1) / BN;
-  const int64_t blocks = max_row_tiles(a.M, a.experts, a.offsets != nullptr, BM) * *panels;
-  return blocks > 0x7FFFFFFF ? 0 : (unsigned)blocks;
-}
+// The kernel of a call, and its grid.
+struct W8a8Grid {
+  W8a8 kind;
+  int BM, BN, threads;
+  int64_t panels, blocks;
+};
 
-template <bool kF32>
-hipError_t launch_w8a8(const I8Args& a, W8a8 kind, hipStream_t st) {
-  int panels = 0;
-  unsigned blocks = 0;
-  auto grid = [&](int BM, int BN) { return (blocks = block_count(a, BM, BN, &panels)) != 0; };
-  switch (kind) {
-    case W8a8::kTile256:
-      if (grid(256, 256)) w8a8_tile_kernel<2, 4, 8, 1, kF32><<<blocks, 512, 0, st>>>(a, panels);
-      break;
+W8a8Grid w8a8_grid(int64_t M, int64_t N, int64_t experts, bool grouped) {
+  W8a8Grid g{choose_w8a8(M, N, experts, grouped), 0, 0, 256, 0, 0};
+  auto tile = [&](int BM, int BN, int threads) {
+    g.BM = BM;
+    g.BN = BN;
+    g.threads = threads;
+  };
+  switch (g.kind) {
+    case W8a8::kTile256: tile(256, 256, 512); break;
     case W8a8::kTile128:
-      if (grid(128, 128)) w8a8_tile_kernel<2, 2, 4, 2, kF32><<<blocks, 256, 0, st>>>(a, panels);
-      break;
-    case W8a8::kDeep128:
-      if (grid(128, 128)) w8a8_deep_kernel<2, 2, 4, 1, kF32><<<blocks, 256, 0, st>>>(a, panels);
-      break;
-    case W8a8::kDeep64x128:
-      if (grid(64, 128)) w8a8_deep_kernel<2, 2, 2, 1, kF32><<<blocks, 256, 0, st>>>(a, panels);
-      break;
-    case W8a8::kDeep64:
-      if (grid(64, 64)) w8a8_deep_kernel<2, 1, 2, 2, kF32><<<blocks, 256, 0, st>>>(a, panels);
-      break;
-    case W8a8::kStream32x64:
-      if (grid(32, 64)) w8a8_stream_kernel<2, 4, 4, false, kF32><<<blocks, 256, 0, st>>>(a);
-      break;
-    case W8a8::kStream16x64:
-      if (grid(16, 64)) w8a8_stream_kernel<1, 4, 4, false, kF32><<<blocks, 256, 0, st>>>(a);
-      break;
+    case W8a8::kDeep128: tile(128, 128, 256); break;
+    case W8a8::kDeep64x128: tile(64, 128, 256); break;
+    case W8a8::kDeep64: tile(64, 64, 256); break;
+    case W8a8::kStream32x64: tile(32, 64, 256); break;
+    case W8a8::kStream16x64: tile(16, 64, 256); break;
     case W8a8::kRows16: {
       // Two row blocks per wavefront once that leaves enough blocks, and K divided
       // between two wavefronts where the row blocks alone fill the GPU, else four
       // (one row: 2560 x 9216 6.6 us as one row block and four wavefronts, 9.0 as two
       // and two; 9216 x 2560 6.6 and 6.4; 5120 x 17408 16.5 as two and four, 19.9 as
       // one and four).
-      const int64_t nb = (a.N + kTileRows - 1) / kTileRows * (a.experts < a.M ? a.experts : a.M);
+      const int64_t nb = (N + kTileRows - 1) / kTileRows * (experts < M ? experts : M);
+      if (nb < 256) tile(16, 16, 256);
+      else tile(16, 32, nb < 512 ? 256 : 128);
+      break;
+    }
+  }
+  g.panels = (N + g.BN - 1) / g.BN;
+  g.blocks = max_row_tiles(M, experts, grouped, g.BM) * g.panels;
+  return g;
+}
+
+template <bool kF32>
+hipError_t launch_w8a8(const I8Args& a, hipStream_t st) {
+  const W8a8Grid g = w8a8_grid(a.M, a.N, a.experts, a.offsets != nullptr);
+  const unsigned blocks = (unsigned)g.blocks;
+  const int panels = (int)g.panels;
+  switch (g.kind) {
+    case W8a8::kTile256:
+      w8a8_tile_kernel<2, 4, 8, 1, kF32><<<blocks, 512, 0, st>>>(a, panels);
+      break;
+    case W8a8::kTile128:
+      w8a8_tile_kernel<2, 2, 4, 2, kF32><<<blocks, 256, 0, st>>>(a, panels);
+      break;
+    case W8a8::kDeep128:
+      w8a8_deep_kernel<2, 2, 4, 1, kF32><<<blocks, 256, 0, st>>>(a, panels);
+      break;
+    case W8a8::kDeep64x128:
+      w8a8_deep_kernel<2, 2, 2, 1, kF32><<<blocks, 256, 0, st>>>(a, panels);
+      break;
+    case W8a8::kDeep64:
+      w8a8_deep_kernel<2, 1, 2, 2, kF32><<<blocks, 256, 0, st>>>(a, panels);
+      break;
+    case W8a8::kStream32x64:
+      w8a8_stream_kernel<2, 4, 4, false, kF32><<<blocks, 256, 0, st>>>(a);
+      break;
+    case W8a8::kStream16x64:
+      w8a8_stream_kernel<1, 4, 4, false, kF32><<<blocks, 256, 0, st>>>(a);
+      break;
+    case W8a8::kRows16: {
       // Weights of 64 MiB or more are read past the caches, which is faster while each call has
       // other weights than the last one (one row, us through the caches and past them: 17408 x 5120
       // 20.4 and 18.2, 8192 x 8192 15.7 and 14.1).  Called again and again, a matrix that the
@@ -813,32 +839,25 @@ hipError_t launch_w8a8(const I8Args& a, W8a8 kind, hipStream_t st) {
       // x 5120 15.9 and 15.0, its 13 rows 17.8 and 18.3).  Below, the threshold leaves up to
       // a tenth to the caches: 8192 x 5120 10.5 and 9.5, again and again 8.0 and 7.7.
       const bool past = (int64_t)a.experts * a.N * a.K >= (int64_t)64 << 20;
-      if (nb < 256) {
-        if (grid(16, 16)) w8a8_stream_kernel<1, 1, 4, false, kF32><<<blocks, 256, 0, st>>>(a);
-      } else if (nb < 512) {
-        if (!grid(16, 32)) break;
-        if (past) w8a8_stream_kernel<1, 2, 4, true, kF32><<<blocks, 256, 0, st>>>(a);
-        else w8a8_stream_kernel<1, 2, 4, false, kF32><<<blocks, 256, 0, st>>>(a);
-      } else {
-        if (!grid(16, 32)) break;
-        if (past) w8a8_stream_kernel<1, 2, 2, true, kF32><<<blocks, 128, 0, st>>>(a);
-        else w8a8_stream_kernel<1, 2, 2, false, kF32><<<blocks, 128, 0, st>>>(a);
-      }
+      if (g.BN == 16) w8a8_stream_kernel<1, 1, 4, false, kF32><<<blocks, 256, 0, st>>>(a);
+      else if (g.threads == 256 && past) w8a8_stream_kernel<1, 2, 4, true, kF32><<<blocks, 256, 0, st>>>(a);
+      else if (g.threads == 256) w8a8_stream_kernel<1, 2, 4, false, kF32><<<blocks, 256, 0, st>>>(a);
+      else if (past) w8a8_stream_kernel<1, 2, 2, true, kF32><<<blocks, 128, 0, st>>>(a);
+      else w8a8_stream_kernel<1, 2, 2, false, kF32><<<blocks, 128, 0, st>>>(a);
       break;
     }
   }
-  return blocks ? hipGetLastError() : hipErrorInvalidConfiguration;
+  return hipGetLastError();
 }
 
 // A wavefront per row while four chunks per lane hold it, else 256 threads with up to
 // 16 chunks each, else 1024.
 template <bool kF32, bool kNative>
-hipError_t launch_quantize_rows(const void* x, int64_t rows, int64_t K, int8_t* q, float* scale, hipStream_t st) {
+hipError_t launch_rows(const void* x, int64_t rows, int64_t K, int8_t* q, float* scale, hipStream_t st) {
   const int64_t padded = kNative ? (rows + kTileRows - 1) / kTileRows * kTileRows : rows;
   const int64_t chunks = K / (kF32 ? 4 : 8);
   // native: whole row blocks for each XCD in turn
   const int64_t all = kNative ? (padded / kTileRows + kXcds - 1) / kXcds * kXcds * kTileRows : rows;
-  if (all > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   const unsigned n = (unsigned)all;
   const int r = (int)rows, p = (int)padded, k = (int)K;
   if (chunks <= 4 * 64)
@@ -854,6 +873,20 @@ hipError_t launch_quantize_rows(const void* x, int64_t rows, int64_t K, int8_t* 
   return hipGetLastError();
 }
 
+// Launches of at most 2^31 threads, whole sets of row blocks each: 64 to 1024 threads a row.
+template <bool kF32, bool kNative>
+hipError_t launch_quantize_rows(const void* x, int64_t rows, int64_t K, int8_t* q, float* scale, hipStream_t st) {
+  const int64_t chunks = K / (kF32 ? 4 : 8);
+  const int64_t most = (kMaxThreads / 2) / (chunks <= 4 * 64 ? 64 : chunks <= 16 * 256 ? 256 : 1024);
+  for (int64_t at = 0; at < rows; at += most) {
+    const int64_t n = rows - at < most ? rows - at : most;
+    const hipError_t e = launch_rows<kF32, kNative>(static_cast<const uint8_t*>(x) + at * K * (kF32 ? 4 : 2), n, K,
+                                                    q + at * K, scale + at, st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 }  // namespace
 
 hipError_t launch_quantize_w8(const float* W, int64_t N, int64_t K, int8_t* q, float* d, hipStream_t stream) {
@@ -867,22 +900,32 @@ hipError_t launch_quantize_tokens(const void* x, bool f32, int64_t M, int64_t K,
 }
 
 hipError_t launch_pack_w8(const int8_t* src, int64_t N, int64_t K, int8_t* dst, bool pack, hipStream_t stream) {
-  const int64_t chunks = (N + kTileRows - 1) / kTileRows * K;  // 16 rows x K codes / 16
-  if (chunks > (int64_t)256 * 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  const unsigned blocks = (unsigned)((chunks + 255) / 256);
-  if (pack)
-    repack_kernel<true><<<blocks, 256, 0, stream>>>(src, N, K, chunks, dst);
-  else
-    repack_kernel<false><<<blocks, 256, 0, stream>>>(src, N, K, chunks, dst);
-  return hipGetLastError();
+  // launches of at most 2^30 threads, whole row blocks each (16 rows x K codes / 16 a thread)
+  const int64_t most = (kMaxThreads / 4) / K * kTileRows;
+  for (int64_t at = 0; at < N; at += most) {
+    const int64_t n = N - at < most ? N - at : most;
+    const int64_t chunks = (n + kTileRows - 1) / kTileRows * K;
+    const unsigned blocks = (unsigned)((chunks + 255) / 256);
+    if (pack)
+      repack_kernel<true><<<blocks, 256, 0, stream>>>(src + at * K, n, K, chunks, dst + at * K);
+    else
+      repack_kernel<false><<<blocks, 256, 0, stream>>>(src + at * K, n, K, chunks, dst + at * K);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+bool fits_linear_w8a8(int64_t M, int64_t N, int64_t experts, bool grouped) {
+  const W8a8Grid g = w8a8_grid(M, N, experts, grouped);
+  return g.blocks * g.threads < kMaxThreads;
 }
 
 hipError_t launch_linear_w8a8(const int8_t* xq, const float* sx, int64_t M, int64_t K, const int32_t* offsets,
                               int64_t experts, const int8_t* q, const float* d, int64_t N, void* y, bool f32,
                               hipStream_t stream) {
   const I8Args a{xq, sx, offsets, q, d, y, (int)M, (int)K, (int)N, (int)experts};
-  const W8a8 kind = choose_w8a8(M, N, experts, offsets != nullptr);
-  return f32 ? launch_w8a8<true>(a, kind, stream) : launch_w8a8<false>(a, kind, stream);
+  return f32 ? launch_w8a8<true>(a, stream) : launch_w8a8<false>(a, stream);
 }
 
 }  // namespace w4

@@ -155,6 +155,9 @@ hipError_t launch_gptq_update(float* W, int64_t N, int64_t K, int64_t b0, const 
 hipError_t launch_dense_linear_f32(const uint16_t* x, int64_t T, int64_t K, const float* W, int64_t N, float* y,
                                    hipStream_t stream);
 
+// A launch takes less than 2^32 threads.
+constexpr int64_t kMaxThreads = int64_t(1) << 32;
+
 // 8-bit integers with token and channel scales (int8.hip).
 hipError_t launch_quantize_w8(const float* W, int64_t N, int64_t K, int8_t* q, float* d, hipStream_t stream);
 // x bf16 (or fp32) [M][K] -> xq int8 [M][K], sx fp32 [M].
@@ -165,12 +168,14 @@ hipError_t launch_pack_w8(const int8_t* src, int64_t N, int64_t K, int8_t* dst, 
 // y = sx d (xq q^T), bf16 or fp32.  offsets (device, experts + 1 values): rows
 // sorted by expert, expert e's weight e native matrices after q and e * N scales
 // after d; nullptr: one matrix for all rows.
+bool fits_linear_w8a8(int64_t M, int64_t N, int64_t experts, bool grouped);  // the tiles fit a launch
 hipError_t launch_linear_w8a8(const int8_t* xq, const float* sx, int64_t M, int64_t K, const int32_t* offsets,
                               int64_t experts, const int8_t* q, const float* d, int64_t N, void* y, bool f32,
                               hipStream_t stream);
 
 // Rows sorted by expert times 4-bit weights (grouped.hip): the native codes and
 // scales of the experts follow each other.
+bool fits_linear_grouped(int64_t M, int64_t N, int64_t experts);
 hipError_t launch_linear_grouped(const uint16_t* x, int64_t M, int64_t K, const int32_t* offsets, int64_t experts,
                                  const uint8_t* q, const void* d, bool s16, int64_t N, void* y, bool f32,
                                  hipStream_t stream);

@@ -681,6 +681,10 @@ w4_status w4_linear_w8a8_f32(const int8_t* xq, const float* sx, int64_t M, int64
  * depend on which other rows and experts the call holds; a 4-bit one may differ
  * in the last bits between calls of different sizes (the kernel is chosen by M,
  * N and experts, and sums in another order).
+ * One launch covers every routing of M rows to the experts.  One that would take
+ * 2^32 threads or more is refused (W4_ERR_SHAPE); none does while
+ * (M / 16 + min(experts, M)) * (N + 63) < 2^30, and a dense 8-bit product none
+ * whose y fits the memory.
  */
 #define W4_MAX_EXPERTS 4096
 

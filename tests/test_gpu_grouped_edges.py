@@ -84,3 +84,47 @@ def test_dominant_inputs_at_zero_codes(w4, gpu, rows, big, scale_dtype):
             for y in ys:
                 ok = oracle.admissible(_bits(y[a:b]), ref, absdot, "f32" if out_dtype == F32 else "bf16", abs_=abs_)
                 assert ok.all(), f"expert {e} {out_dtype}: {int((~ok).sum())} of {ok.size} outputs out of tolerance"
+
+
+# ----------------------------------------------------------------------------
+# more rows than one launch takes
+# ----------------------------------------------------------------------------
+
+def test_quantize_w8_rows_past_one_launch(w4, gpu):
+    """2^25 rows of 128 inputs fill a launch: the rows around its end, and the last ones, bit for bit."""
+    N, K = (1 << 25) + 1037, 128
+    _say(f"quantize_w8 {N} x {K}")
+    W = torch.empty((N, K), device=gpu)
+    g = torch.Generator(device=gpu)
+    g.manual_seed(5)
+    W.normal_(generator=g)
+    q, d = w4.quantize_w8(W)
+    assert bool(torch.isfinite(d).all()) and bool((d > 0).all())
+    for a, b in ((0, 160), ((1 << 25) - 160, (1 << 25) + 160), ((1 << 25) + 1008, N)):  # (a: whole row blocks)
+        q_ref, d_ref = oracle.rtn_rows_ref(W[a:b].cpu().numpy())
+        assert np.array_equal(d[a:b].cpu().numpy().view(np.uint32), d_ref.view(np.uint32)), "scales differ"
+        packed = oracle.pack_w8_ref(q_ref)
+        assert np.array_equal(q[a * K:a * K + packed.size].cpu().numpy(), packed), "codes differ"
+    want, most = torch.empty_like(d), torch.full((1,), 127.0, device=gpu)
+    for a in range(0, N, 1 << 22):  # every scale
+        want[a:a + (1 << 22)] = W[a:a + (1 << 22)].abs().amax(dim=1) / most
+    assert torch.equal(d, want)
+
+
+def test_pack_w8_rows_past_one_launch(w4, gpu):
+    """2^30 chunks of 16 codes fill a launch: every code goes there and back, and the layout around the
+    launch's end is the oracle's."""
+    N, K = (1 << 27) + 1037, 128
+    _say(f"pack_w8 {N} x {K}")
+    c = torch.empty((N, K), dtype=torch.int8, device=gpu)
+    g = torch.Generator(device=gpu)
+    g.manual_seed(6)
+    for a in range(0, N, 1 << 24):
+        c[a:a + (1 << 24)].random_(-128, 128, generator=g)
+    q = w4.pack_w8(c)
+    for a, b in ((0, 160), ((1 << 27) - 160, (1 << 27) + 160), ((1 << 27) + 1008, N)):
+        packed = oracle.pack_w8_ref(c[a:b].cpu().numpy())
+        assert np.array_equal(q[a * K:a * K + packed.size].cpu().numpy(), packed), "layout differs"
+    back = w4.unpack_w8(q, N, K)
+    for a in range(0, N, 1 << 24):
+        assert torch.equal(back[a:a + (1 << 24)], c[a:a + (1 << 24)])

@@ -6,6 +6,8 @@ import numpy as np
 
 import oracle
 
+OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_HIP, ERR_ARG = range(6)
+
 
 def test_offset_scale_ref_against_fractions():
     rng = np.random.default_rng(1)
@@ -48,3 +50,36 @@ def test_rounding_of_a_group_formed_with_an_offset():
         worst_q = max(worst_q, err / (2e-3 * np.abs(q * x).sum() + 1e-6))
     assert worst <= oracle.OFFSET_TOL
     assert worst_q > 1.0  # the term is there for a reason
+
+
+def test_calls_of_too_many_threads_are_refused(w4):
+    """A grid of 2^32 threads or more cannot be launched: refused as a shape before anything else is looked
+    at, and never while (M / 16 + min(experts, M)) * (N + 63) < 2^30."""
+    lib = w4.library()
+    names = ("w4_linear_grouped", "w4_linear_grouped_f32_s16", "w4_linear_grouped_w8a8", "w4_linear_grouped_w8a8_f32")
+
+    def call(name, M, N, E):
+        x, off, K = 0x10000000, 0x20000000, 128
+        args = [x, x, M, K, off, E] if "w8a8" in name else [x, M, K, off, E]
+        return getattr(lib, name)(*args, None, x, N, x, None)  # no codes: an error of its own once the shape is taken
+
+    for name in names:
+        # 6144 (8-bit: 5632) row tiles of 16 rows
+        w8 = "w8a8" in name
+        M, E = (24576, 4096) if w8 else (32768, 4096)
+        per = 4 if w8 else 2  # threads per row tile and output
+        tiles = M // 16 + E
+        N = (1 << 32) // (per * tiles) // 64 * 64
+        assert call(name, M, N + 128, E) == ERR_SHAPE
+        assert call(name, M, N - 128, E) == ERR_NULL
+    rng = np.random.default_rng(5)
+    for _ in range(3000):
+        M, E = int(2 ** rng.uniform(0, 18)), int(2 ** rng.uniform(0, 12))
+        most = min(((1 << 30) - 1) // (M // 16 + min(E, M)) - 63, (1 << 23) - 16)
+        N = int(most * rng.choice([1.0, rng.uniform(0, 1)]))
+        if N > 0:
+            assert call(names[_ % 4], M, N, E) == ERR_NULL, (M, N, E)
+    for _ in range(3000):  # dense 8-bit products: up to 400 GB of y
+        M = int(2 ** rng.uniform(0, 18))
+        N = min(int(2e11 / M), (1 << 24) - 16)
+        assert lib.w4_linear_w8a8(0x10000000, 0x10000000, M, 128, None, 0x10000000, N, 0x10000000, None) == ERR_NULL, (M, N)
