@@ -799,6 +799,8 @@ class W8Linear:
 
     @classmethod
     def from_float(cls, W):
+        if not isinstance(W, torch.Tensor) or W.dim() != 2:
+            raise TypeError("W must be a 2-D torch.Tensor")
         q, d = quantize_w8(W)
         return cls(q, d, W.shape[0], W.shape[1])
 

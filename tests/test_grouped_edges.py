@@ -3,6 +3,8 @@
 from fractions import Fraction
 
 import numpy as np
+import pytest
+import torch
 
 import oracle
 
@@ -83,3 +85,9 @@ def test_calls_of_too_many_threads_are_refused(w4):
         M = int(2 ** rng.uniform(0, 18))
         N = min(int(2e11 / M), (1 << 24) - 16)
         assert lib.w4_linear_w8a8(0x10000000, 0x10000000, M, 128, None, 0x10000000, N, 0x10000000, None) == ERR_NULL, (M, N)
+
+
+@pytest.mark.parametrize("shape", [(1, 16, 128), (3, 16, 128), (128,)])
+def test_w8linear_takes_one_matrix(w4, shape):
+    with pytest.raises(TypeError, match="2-D"):
+        w4.W8Linear.from_float(torch.zeros(shape))
