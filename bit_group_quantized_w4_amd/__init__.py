@@ -782,6 +782,9 @@ def grouped_linear(x, offsets, q, d, N, out=None, out_dtype=torch.bfloat16):
     dev, M, K = _rows(x, (torch.bfloat16,), "x")
     sd = _scale_dtype(d)
     nb, ns = _packed_sizes(N, K)
+    # (two experts of K inputs take as many bytes as four of K / 2)
+    if isinstance(q, torch.Tensor) and q.dim() == 2 and q.shape[0] != E:
+        raise ValueError(f"offsets are of {E} experts, q of {q.shape[0]}")
     y, f32 = _output(out, out_dtype, M, N, x.device)
     name = "w4_linear_grouped" + ("_f32" if f32 else "") + ("_s16" if sd == torch.bfloat16 else "")
     _launch(name, dev, x.data_ptr(), M, K, _ptr(offsets, torch.int32, dev, "offsets"), E,

@@ -128,3 +128,12 @@ def test_pack_w8_rows_past_one_launch(w4, gpu):
     back = w4.unpack_w8(q, N, K)
     for a in range(0, N, 1 << 24):
         assert torch.equal(back[a:a + (1 << 24)], c[a:a + (1 << 24)])
+
+
+def test_grouped_linear_refuses_another_number_of_experts(w4, gpu):
+    """Four experts of 512 inputs take as many bytes as two of 1024, which x and the offsets ask for."""
+    _say("grouped_linear, four experts for offsets of two")
+    _, q, d = _w4_experts(w4, gpu, 61, 4, 32, 512, F32)
+    x = workloads.random_activations(6, 1024, seed=61, device=gpu)
+    with pytest.raises(ValueError, match="experts"):
+        w4.grouped_linear(x, torch.tensor([0, 2, 6], dtype=torch.int32, device=gpu), q, d, 32)
