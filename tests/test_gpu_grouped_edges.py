@@ -137,3 +137,67 @@ def test_grouped_linear_refuses_another_number_of_experts(w4, gpu):
     x = workloads.random_activations(6, 1024, seed=61, device=gpu)
     with pytest.raises(ValueError, match="experts"):
         w4.grouped_linear(x, torch.tensor([0, 2, 6], dtype=torch.int32, device=gpu), q, d, 32)
+
+
+# ----------------------------------------------------------------------------
+# scale and output types; rows that do not disturb each other
+# ----------------------------------------------------------------------------
+
+def _check_experts(w4, gpu, W, q, d, sizes, first, extra, N, K, scale_dtype, out_dtype, seed):
+    off = _offsets(sizes, first)
+    M = first + sum(sizes) + extra
+    x = workloads.random_activations(M, K, seed=seed, device=gpu)
+    y = torch.full((M, N), 7.0, dtype=out_dtype, device=gpu)
+    w4.grouped_linear(x, torch.from_numpy(off).to(gpu), q, d, N, out=y)
+    for e, (a, b) in enumerate(zip(off[:-1], off[1:])):
+        if a < b:
+            ref, absdot = _w4_ref(W[e].cpu().numpy(), _bits(x)[a:b], scale_dtype)
+            check_w4(y[a:b], ref, absdot, f"expert {e}")
+    assert bool((y[:first] == 7.0).all()) and bool((y[off[-1]:] == 7.0).all()), "a row of no expert was written"
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("si", range(len(SIZES)))
+def test_grouped_linear_scales_typed_as_outputs(w4, gpu, si, dtype):
+    """bf16 scales with bf16 outputs and fp32 with fp32: streamed, 32-row and 64-row tiles."""
+    N, K = [(33, 256), (130, 640), (513, 128)][si % 3]
+    _say(f"grouped_linear sizes={SIZES[si][:6]} N={N} K={K} scales and outputs {dtype}")
+    W, q, d = _w4_experts(w4, gpu, 70 + si, len(SIZES[si]), N, K, dtype)
+    first, extra = (2, 3) if si % 2 else (0, 0)
+    _check_experts(w4, gpu, W, q, d, SIZES[si], first, extra, N, K, dtype, dtype, si)
+
+
+# Streamed with four row blocks per wavefront, 32-row and 64-row tiles of several panels.
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("N,K,sizes", [(2050, 256, [3, 0] * 11 + [7, 8, 1] * 4), (1000, 4224, [40, 8, 0, 33]),
+                                       (2304, 1152, [290, 0, 45])])
+def test_grouped_linear_larger_scales_typed_as_outputs(w4, gpu, N, K, sizes, dtype):
+    _say(f"grouped_linear N={N} K={K} sizes={sizes[:6]} scales and outputs {dtype}")
+    W, q, d = _w4_experts(w4, gpu, 90, len(sizes), N, K, dtype)
+    _check_experts(w4, gpu, W, q, d, sizes, 0, 0, N, K, dtype, dtype, 90)
+
+
+@pytest.mark.parametrize("M", [20, 120, 600])
+def test_grouped_linear_rows_are_independent(w4, gpu, M):
+    """Within calls of one size (M, N and experts choose the kernel) a 4-bit row's bits depend on its own
+    values and its own expert alone: not on the other rows' values, nor on how these are routed, nor
+    on where in the call the row stands."""
+    _say(f"grouped_linear rows beside others, M={M}")
+    E, N, K = 4, 200, 1152
+    _, q, d = _w4_experts(w4, gpu, 51, E, N, K, BF16)
+    rng = np.random.default_rng(M)
+    mine = workloads.random_activations(3, K, seed=51, device=gpu)  # rows of expert 2
+
+    def run(before, own, at, seed):
+        """before rows of experts 0 and 1, `own` of expert 2 with `mine` from its row `at` on, the rest expert 3's"""
+        x = workloads.random_activations(M, K, seed=seed, device=gpu)
+        x[before + at:before + at + 3] = mine
+        if seed % 2:
+            x[before + own - 1] = float("nan")  # the last row of the expert: another tile's or the same one's
+        off = torch.tensor([0, int(rng.integers(0, before + 1)), before, before + own, M], dtype=torch.int32, device=gpu)
+        return w4.grouped_linear(x, off, q, d, N, out_dtype=F32)[before + at:before + at + 3]
+
+    want = run(0, 4, 0, 2)
+    assert bool(torch.isfinite(want).all())
+    for before, own, at, seed in ((0, 4, 0, 3), (5, 9, 2, 4), (M // 2, 5, 1, 5), (3, M - 3, M - 10, 7), (M - 6, 6, 2, 8)):
+        assert same_bits(run(before, own, at, seed), want)
