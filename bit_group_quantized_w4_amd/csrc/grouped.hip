@@ -164,7 +164,7 @@ __global__ __launch_bounds__(NW * 64) void grouped_stream_kernel(const GroupedAr
 // x goes to LDS straight from memory, two steps ahead, in three buffers.  Lane l of
 // a load takes row l / 16 of four and its 16-byte chunk (l % 16) ^ (row % 16), so
 // that the sixteen rows of an operand are read without bank conflicts.  Codes go
-// straight to registers (each is used by two wavefronts only) and are widened
+// straight to registers (each is used by one of the block's wavefronts) and are widened
 // there.
 //
 // The partial sums of a group start from -1.5 * (sum of its x), which depends on the
@@ -178,11 +178,11 @@ __global__ __launch_bounds__(NW * 64) void grouped_stream_kernel(const GroupedAr
 // codes and the loads.  The barrier of a step stands before the last tile's products
 // of the group before: beside these the operands of the new group are read.
 //
-// 8190 rows of eight experts, 9216 x 2560: 390 us (990 TFLOP/s; up to 425 us where the
-// power limit lowers the clock).  Bound by the issue of
-// vector instructions: an MFMA takes about nine of its sixteen cycles to issue and
-// each vector instruction four more, of which there are 2.9 per MFMA (widening 1.75,
-// accumulation 1).  64 rows per block (two blocks of four wavefronts per CU, whose
+// 8190 rows of eight experts, 9216 x 2560: 381 to 390 us (1000 TFLOP/s at 1.94 GHz; up to
+// 425 us where the power limit lowers the clock further).  Bound by the issue of vector
+// instructions: beside each MFMA there are 3.3 (1.65 widen codes, 0.94 accumulate, the rest
+// are addresses and loads), four cycles each, and the matrix units, sixteen cycles an
+// MFMA, are busy in 62% of the cycles that a CU has work.  64 rows per block (two blocks of four wavefronts per CU, whose
 // barriers do not wait for each other) beat 128 rows in one block of eight (437 us).
 //
 // Steps past the last group (there are up to two, for the three buffers) read zeros (see

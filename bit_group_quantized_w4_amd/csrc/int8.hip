@@ -84,8 +84,9 @@ __device__ __forceinline__ uint32_t max_bits(const uint4& c, uint32_t m) {
 // its low bits, in one fma.  v * y is within 127.5 * 2^-24 of v / d, and the IEEE quotient
 // that the code is defined by within 2^-18 of it: together less than 2^-16, so the
 // code is the same unless v * y lies that near to a half-integer.  Where a thread
-// of the wavefront finds one of its chunk's values within 2^-15 of a half (3% of chunks
-// of normal weights), or the scale lies outside [2^-100, 2^100], the chunk's codes are
+// of the wavefront finds one of its chunk's values within 2^-15 of a half (a share of 2^-14
+// of the values: 1.6% of the wavefront's fp32 chunks of 256 values, 3% of its bf16 ones of
+// 512), or the scale lies outside [2^-100, 2^100], the chunk's codes are
 // formed from the IEEE quotients.
 //
 // Bound by memory: 28672 x 8192 weights (1.17 GB) take 232 us (5.1 TB/s; a copy
@@ -434,8 +435,9 @@ __global__ __launch_bounds__(NW * 64) void w8a8_stream_kernel(const I8Args a) {
 // load holds up the wavefront for the 16 cycles that the address unit of the CU
 // takes for it, which eight wavefronts would otherwise spend in turn before any
 // product (4096 rows of 17408 x 5120: 361 us with all reads and loads first, 338
-// with both spread).  Now 313 to 329 us, 2.2 to 2.3 POP/s, by the clock that the power
-// limit leaves at that rate.
+// with both spread).  Now 310 to 329 us, 2.2 to 2.4 POP/s: the clock falls from 2.4 to
+// 2.04 GHz at that rate, the 1088 tiles fill 81% of five rounds of 256 CUs, and the
+// matrix units are busy in 65% of the cycles that a CU has a tile.
 //
 // Rows past the tile's last, row blocks past the matrix's last and steps past the
 // last one lie outside their buffers: such loads give zeros (see kOob).
@@ -579,8 +581,9 @@ __global__ __launch_bounds__(WM* WN * 64, OCC) void w8a8_tile_kernel(const I8Arg
 // operand reads free of bank conflicts (LDS serves lanes 0-3, 12-15 and 20-27 of
 // a 16-byte read together).  333 rows of 2561 x 9216: 21 us with 64 x 64 tiles and
 // two groups, 43 us as 128 x 128 tiles of the kernel above.  Bound by what L2 delivers: a
-// block alone takes 0.12 us per 128 inputs, 246 of them at once 0.24 us (16 TB/s); four
-// groups, twice the loads in flight, take 1 us longer.
+// block alone takes 0.12 us per 128 inputs, 246 of them at once 0.24 us; together they load
+// 290 MB (14 TB/s, 77% of the requests hits), and the matrix units are busy in 24% of
+// the cycles; four groups, twice the loads in flight, take 1 us longer.
 __device__ __forceinline__ uint32_t quad_swizzle(int t) { return (0x78u >> (2 * t)) & 3u; }
 
 template <int WM, int WN, int TM, int G, bool kF32>
