@@ -724,10 +724,14 @@ enum class W8a8 { kTile256, kTile128, kDeep128, kDeep64x128, kDeep64, kStream32x
 
 // The kernel for M rows shared out over `experts` matrices of N x K (their true
 // sizes are on the GPU: all are taken to be as busy as the average one).  Up to 16
-// rows each the weight stream is all there is to do; where an average of more than 12
-// means that many experts have more than 16, two row tiles per block read the weights of
-// those once (1024 rows of 64 experts of 1408 x 2560: 50.1 us against 58.6; 720 rows of 64 of
-// 2048 x 2048 49.8 and 50.9, but 88 rows of 8 of 2560 x 2560 13.5 and 11.9).  Beyond that the smallest
+// rows each the weight stream is all there is to do.  Of grouped calls with 13 to 16 rows per
+// expert on average many have experts with more than 16; two row tiles per block read the
+// weights of those once.  There neither form is best everywhere (us, 16 and 32 rows per
+// block, popularity as 1 / sqrt(rank): 1024 rows of 64 experts of 1408 x 2560 53.8 and 50.7, of
+// 2048 x 2048 51.6 and 49.0, 128 of 8 of 14336 x 4096 92.1 and 85.7; but 128 of 8 of 2560 x 2560
+// 15.7 and 16.6, 512 of 32 of 2560 x 1408 27.2 and 29.1, and 16 rows for each expert 76.2 and
+// 87.2 at 14336 x 4096), up to 12 the first nearly is (640 rows of the 64 experts of 2048 x
+// 2048 45.5 and 48.1, 96 of 8 of 14336 x 4096 79.4 and 86.3).  Beyond that the smallest
 // estimate wins, in us per 128 inputs, from times measured on the 2560 x 9216,
 // 9216 x 2560, 28672 x 8192 and 17408 x 5120 matrices at 32 to 4096 rows: `one` while
 // every block has a CU for itself, `all` for each further full set of `slots` blocks.
