@@ -436,8 +436,8 @@ __global__ __launch_bounds__(NW * 64) void w8a8_stream_kernel(const I8Args a) {
 // takes for it, which eight wavefronts would otherwise spend in turn before any
 // product (4096 rows of 17408 x 5120: 361 us with all reads and loads first, 338
 // with both spread).  Now 310 to 329 us, 2.2 to 2.4 POP/s: the clock falls from 2.4 to
-// 2.04 GHz at that rate, the 1088 tiles fill 81% of five rounds of 256 CUs, and the
-// matrix units are busy in 65% of the cycles that a CU has a tile.
+// 2.04 GHz at that rate, a CU has a tile 81% of the time (1088 tiles are five rounds of 256,
+// the last a quarter full), and the matrix units are busy in 65% of those cycles.
 //
 // Rows past the tile's last, row blocks past the matrix's last and steps past the
 // last one lie outside their buffers: such loads give zeros (see kOob).
