@@ -200,20 +200,20 @@ def _pad_rows(q, rows):
 
 
 def _native(codes, scales):
-    """Codes [.., N, K / 2] as tiles of 16 rows x 64 bytes (lane L of a tile: row L % 16, bytes 16 (L // 16) .. + 15)
-    and scales [.., N, K / 32] as words: a word for each tile lane holds the scales of its row's blocks in four
-    consecutive tiles along K (lane L's block of tile t is 4 t + L // 16), zeros past the last."""
-    N = codes.shape[-2]
-    rows, lead = (N + 15) // 16 * 16, codes.shape[:-2]
-    n = len(lead)
+    """Codes [.., N, K / 2] as tiles of 16 rows x 64 bytes, two for every 256 inputs: lane L of the two holds row
+    L % 16, inputs 64 (L // 16) .. + 63, a block of 32 in each.  Scales [.., N, K / 32] as four bytes for each lane
+    and 512 inputs, in the order of its blocks.  Zeros past the last row and input."""
+    N, lead = codes.shape[-2], codes.shape[:-2]
+    rows, n = (N + 15) // 16 * 16, codes.dim() - 2
+    pad = torch.nn.functional.pad
     q = _pad_rows(codes, rows)
-    q = q.reshape(lead + (rows // 16, 16, q.shape[-1] // 64, 4, 16))
-    q = q.permute(tuple(range(n)) + (n, n + 2, n + 3, n + 1, n + 4)).reshape(lead + (-1,)).contiguous()
+    q = pad(q, (0, -q.shape[-1] % 128))
+    q = q.reshape(lead + (rows // 16, 16, q.shape[-1] // 128, 4, 2, 16))  # row, 256 inputs, quarter, block, byte
+    q = q.permute(tuple(range(n)) + (n, n + 2, n + 4, n + 3, n + 1, n + 5)).reshape(lead + (-1,)).contiguous()
     s = _pad_rows(scales, rows)
-    blocks = (s.shape[-1] + 15) // 16 * 16
-    s = torch.nn.functional.pad(s, (0, blocks - s.shape[-1]))
-    s = s.reshape(lead + (rows // 16, 16, blocks // 16, 4, 4))  # row, word of a row, tile, lane's block
-    s = s.permute(tuple(range(n)) + (n, n + 2, n + 4, n + 1, n + 3)).reshape(lead + (-1,)).contiguous()
+    s = pad(s, (0, -s.shape[-1] % 16))
+    s = s.reshape(lead + (rows // 16, 16, s.shape[-1] // 16, 2, 4, 2))  # row, 512 inputs, half, quarter, block
+    s = s.permute(tuple(range(n)) + (n, n + 2, n + 4, n + 1, n + 3, n + 5)).reshape(lead + (-1,)).contiguous()
     return q, s
 
 
