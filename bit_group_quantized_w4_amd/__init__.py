@@ -10,6 +10,7 @@ been built (build it with ``python -m bit_group_quantized_w4_amd._build``).
 
 import ctypes
 import os
+import typing
 
 import torch
 
@@ -22,6 +23,8 @@ GROUP = 128
 
 _VP, _I64, _INT, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 MAX_BATCH = 64
+MAX_EXPERTS = 4096
+MAX_SLOTS = 262140
 
 
 class LinearDesc(ctypes.Structure):
@@ -118,6 +121,31 @@ SIGNATURES = {
     "w4_linear_grouped_f32_s16": (_INT, [_VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP]),
     "w4_linear_grouped_w8a8": (_INT, [_VP, _VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP]),
     "w4_linear_grouped_w8a8_f32": (_INT, [_VP, _VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP]),
+    # microscaled 4-bit floating point
+    "w4_mx4_packed_bytes": (_SZ, [_I64, _I64]),
+    "w4_mx4_scale_bytes": (_SZ, [_I64, _I64]),
+    "w4_quantize_mx4": (_INT, [_VP, _I64, _I64, _VP, _VP, _VP]),
+    "w4_quantize_mx4_f32": (_INT, [_VP, _I64, _I64, _VP, _VP, _VP]),
+    "w4_dequantize_mx4": (_INT, [_VP, _VP, _I64, _I64, _VP, _VP]),
+    "w4_dequantize_mx4_f32": (_INT, [_VP, _VP, _I64, _I64, _VP, _VP]),
+    "w4_pack_mx4": (_INT, [_VP, _VP, _I64, _I64, _VP, _VP, _VP]),
+    "w4_unpack_mx4": (_INT, [_VP, _VP, _I64, _I64, _VP, _VP, _VP]),
+    "w4_quantize_tokens_mx4": (_INT, [_VP, _I64, _I64, _VP, _VP, _VP]),
+    "w4_quantize_tokens_mx4_f32": (_INT, [_VP, _I64, _I64, _VP, _VP, _VP]),
+    "w4_dequantize_tokens_mx4": (_INT, [_VP, _VP, _I64, _I64, _VP, _VP]),
+    "w4_dequantize_tokens_mx4_f32": (_INT, [_VP, _VP, _I64, _I64, _VP, _VP]),
+    "w4_linear_mx4": (_INT, [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _VP, _VP]),
+    "w4_linear_mx4_f32": (_INT, [_VP, _VP, _I64, _I64, _VP, _VP, _I64, _VP, _VP]),
+    "w4_linear_grouped_mx4": (_INT, [_VP, _VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP]),
+    "w4_linear_grouped_mx4_f32": (_INT, [_VP, _VP, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP]),
+    # rows to the experts and back
+    "w4_expert_sort_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "w4_expert_sort": (_INT, [_VP, _INT, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "w4_expert_take": (_INT, [_VP, _I64, _I64, _I64, _VP, _I64, _VP, _VP, _VP]),
+    "w4_expert_dispatch": (_INT, [_VP, _I64, _VP, _INT, _I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "w4_expert_combine": (_INT, [_VP, _INT, _VP, _INT, _I64, _I64, _I64, _VP, _VP, _INT, _VP]),
+    "w4_expert_combine_backward": (_INT, [_VP, _INT, _VP, _INT, _VP, _INT, _I64, _I64, _I64, _VP, _I64, _VP, _VP, _VP,
+                                          _VP]),
 }
 
 
@@ -793,6 +821,374 @@ def grouped_linear(x, offsets, q, d, N, out=None, out_dtype=torch.bfloat16):
     return y
 
 
+# ----------------------------------------------------------------------------
+# microscaled 4-bit floating point
+# ----------------------------------------------------------------------------
+
+def packed_bytes_mx4(N, K):
+    """Bytes of the native 4-bit floating-point codes of an N x K matrix (w4_mx4_packed_bytes); 0 for a
+    shape that these functions do not take."""
+    return int(_lib.w4_mx4_packed_bytes(N, K))
+
+
+def scale_bytes_mx4(N, K):
+    """Bytes of their native scales (w4_mx4_scale_bytes)."""
+    return int(_lib.w4_mx4_scale_bytes(N, K))
+
+
+def _sizes_mx4(N, K):
+    """(packed_bytes_mx4, scale_bytes_mx4), refusing a bad shape."""
+    if N >= 0 and 0 < K <= 130944 and K % GROUP == 0:
+        rows = (N + 15) // 16 * 16
+        return rows * ((K + 255) // 256 * 128), rows * ((K + 511) // 512 * 16)
+    _check(W4_ERR_SHAPE, "w4_mx4_packed_bytes")
+
+
+def _wide(name, dtype):
+    """The entry point of `name` for bf16 or fp32 values."""
+    return name + "_f32" if dtype == torch.float32 else name
+
+
+def quantize_mx4(W, out=None):
+    """Weight [N, K] (bf16, or fp32) on the GPU -> (codes uint8 [packed_bytes_mx4(N, K)], scales uint8
+    [scale_bytes_mx4(N, K)]) in the native layout: 4-bit floating point (E2M1) with one power-of-two scale
+    (E8M0) per 32 inputs.  A stack of experts [E, N, K] gives codes and scales with a leading E."""
+    if not isinstance(W, torch.Tensor) or W.dim() not in (2, 3):
+        raise TypeError("W must be a 2-D (or, for experts, 3-D) torch.Tensor")
+    dev, shape = _first(W, OUT_DTYPES, "W")
+    lead, (N, K) = shape[:-2], shape[-2:]
+    nb, ns = _sizes_mx4(N, K)
+    if out is None:
+        out = (torch.empty(lead + (nb,), dtype=torch.uint8, device=W.device),
+               torch.empty(lead + (ns,), dtype=torch.uint8, device=W.device))
+    q, s = out
+    pq, ps, pw = _ptr(q, torch.uint8, dev, "q", lead + (nb,)), _ptr(s, torch.uint8, dev, "s", lead + (ns,)), W.data_ptr()
+    name, size = _wide("w4_quantize_mx4", W.dtype), N * K * W.element_size()
+    if lead and N % 16 == 0:  # row blocks of consecutive experts follow each other: one matrix
+        lead, N = (), N * lead[0]
+    for e in range(lead[0] if lead else 1):
+        _launch(name, dev, pw + e * size, N, K, pq + e * nb, ps + e * ns)
+    return q, s
+
+
+def dequantize_mx4(q, s, N, K, out=None, out_dtype=torch.bfloat16):
+    """The values [N, K] of native codes and scales (NaN where a scale is 255), bf16 or, with
+    out_dtype=torch.float32 (or an fp32 `out`), fp32; exact in both."""
+    dev, _ = _first(q, (torch.uint8,), "q")
+    nb, ns = _sizes_mx4(N, K)
+    pq, ps = _ptr(q, torch.uint8, dev, "q", count=nb), _ptr(s, torch.uint8, dev, "s", count=ns)
+    W, _ = _output(out, out_dtype, N, K, q.device)
+    _launch(_wide("w4_dequantize_mx4", W.dtype), dev, pq, ps, N, K, _ptr(W, W.dtype, dev, "out", (N, K)))
+    return W
+
+
+def pack_mx4(q_canon, s_canon, out=None):
+    """Row-major codes uint8 [N, K / 2] (input k in the low (even k) or high four bits of byte k / 2) and
+    scales uint8 [N, K / 32] -> native (q, s)."""
+    dev, N, half = _rows(q_canon, (torch.uint8,), "q_canon")
+    K = 2 * half
+    nb, ns = _sizes_mx4(N, K)
+    if out is None:
+        out = (torch.empty(nb, dtype=torch.uint8, device=q_canon.device),
+               torch.empty(ns, dtype=torch.uint8, device=q_canon.device))
+    q, s = out
+    _launch("w4_pack_mx4", dev, q_canon.data_ptr(), _ptr(s_canon, torch.uint8, dev, "s_canon", (N, K // 32)), N, K,
+            _ptr(q, torch.uint8, dev, "q", count=nb), _ptr(s, torch.uint8, dev, "s", count=ns))
+    return q, s
+
+
+def unpack_mx4(q, s, N, K):
+    """Native (q, s) -> row-major codes uint8 [N, K / 2] and scales uint8 [N, K / 32]."""
+    dev, _ = _first(q, (torch.uint8,), "q")
+    nb, ns = _sizes_mx4(N, K)
+    pq, ps = _ptr(q, torch.uint8, dev, "q", count=nb), _ptr(s, torch.uint8, dev, "s", count=ns)
+    qc = torch.empty((N, K // 2), dtype=torch.uint8, device=q.device)
+    sc = torch.empty((N, K // 32), dtype=torch.uint8, device=q.device)
+    _launch("w4_unpack_mx4", dev, pq, ps, N, K, qc.data_ptr(), sc.data_ptr())
+    return qc, sc
+
+
+def quantize_tokens_mx4(x, out=None):
+    """Activations [M, K] (bf16, or fp32) -> row-major (xq uint8 [M, K / 2], xs uint8 [M, K / 32])."""
+    dev, M, K = _rows(x, OUT_DTYPES, "x")
+    _sizes_mx4(0, K)
+    if out is None:
+        xq = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+        xs = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
+    else:
+        xq, xs = out
+    _launch(_wide("w4_quantize_tokens_mx4", x.dtype), dev, x.data_ptr(), M, K,
+            _ptr(xq, torch.uint8, dev, "xq", (M, K // 2)), _ptr(xs, torch.uint8, dev, "xs", (M, K // 32)))
+    return xq, xs
+
+
+def dequantize_tokens_mx4(xq, xs, out=None, out_dtype=torch.bfloat16):
+    """The values [M, K] of row-major codes and scales, as dequantize_mx4."""
+    dev, M, half = _rows(xq, (torch.uint8,), "xq")
+    K = 2 * half
+    _sizes_mx4(0, K)
+    x, _ = _output(out, out_dtype, M, K, xq.device)
+    _launch(_wide("w4_dequantize_tokens_mx4", x.dtype), dev, xq.data_ptr(),
+            _ptr(xs, torch.uint8, dev, "xs", (M, K // 32)), M, K, _ptr(x, x.dtype, dev, "out", (M, K)))
+    return x
+
+
+def linear_mx4(xq, xs, q, s, N, out=None, out_dtype=torch.bfloat16):
+    """y [M, N] = x^ w^T over the values of row-major activations (xq uint8 [M, K / 2], xs uint8 [M, K / 32]) and
+    native weights (q, s), accumulated in fp32.  y is bf16, or fp32 with out_dtype=torch.float32 (or an fp32
+    `out`)."""
+    dev, M, half = _rows(xq, (torch.uint8,), "xq")
+    K = 2 * half
+    nb, ns = _sizes_mx4(N, K)
+    y, f32 = _output(out, out_dtype, M, N, xq.device)
+    _launch("w4_linear_mx4_f32" if f32 else "w4_linear_mx4", dev, xq.data_ptr(),
+            _ptr(xs, torch.uint8, dev, "xs", (M, K // 32)), M, K, _ptr(q, torch.uint8, dev, "q", count=nb),
+            _ptr(s, torch.uint8, dev, "s", count=ns), N, _ptr(y, y.dtype, dev, "out", (M, N)))
+    return y
+
+
+def grouped_linear_mx4(xq, xs, offsets, q, s, N, out=None, out_dtype=torch.bfloat16):
+    """linear_mx4 with rows sorted by expert: rows offsets[e] .. offsets[e + 1] - 1 of xq use expert e's
+    weight (q [E, packed_bytes_mx4(N, K)], s [E, scale_bytes_mx4(N, K)], as quantize_mx4 gives them; offsets
+    int32 [E + 1] on the GPU).  Rows of y that no expert owns are left as they were (undefined without
+    `out`)."""
+    E = _experts(offsets)
+    dev, M, half = _rows(xq, (torch.uint8,), "xq")
+    K = 2 * half
+    nb, ns = _sizes_mx4(N, K)
+    y, f32 = _output(out, out_dtype, M, N, xq.device)
+    _launch("w4_linear_grouped_mx4_f32" if f32 else "w4_linear_grouped_mx4", dev, xq.data_ptr(),
+            _ptr(xs, torch.uint8, dev, "xs", (M, K // 32)), M, K, _ptr(offsets, torch.int32, dev, "offsets"), E,
+            _ptr(q, torch.uint8, dev, "q", (E, nb)), _ptr(s, torch.uint8, dev, "s", (E, ns)), N,
+            _ptr(y, y.dtype, dev, "out", (M, N)))
+    return y
+
+
+# ----------------------------------------------------------------------------
+# rows to the experts and back
+# ----------------------------------------------------------------------------
+
+class ExpertRows(typing.NamedTuple):
+    """Slots (a token's choices of experts) sorted by expert, all int32 on the GPU: expert e has rows
+    offsets[e] .. offsets[e + 1] - 1 (offsets [E + 1]); place [T, top] is the row of a slot, -1 for one of no
+    expert; order [T * top] is the slot of a row, -1 from row offsets[E] on."""
+
+    offsets: torch.Tensor
+    place: torch.Tensor
+    order: torch.Tensor
+
+
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}  # w4_type
+_ROW_DTYPES = (torch.bfloat16, torch.float32, torch.uint8, torch.int8)
+
+
+def _ids(experts, E):
+    """Checks the expert ids of a sort: (GPU index, T, top, bytes per id)."""
+    dev, T, top = _rows(experts, (torch.int64, torch.int32), "experts")
+    if not 0 <= E <= MAX_EXPERTS or top < 1 or T * top > MAX_SLOTS:
+        _check(W4_ERR_SHAPE, "w4_expert_sort")
+    return dev, T, top, experts.element_size()
+
+
+def _empty_rows(T, top, E, device):
+    """(ExpertRows to be filled, workspace, its bytes)."""
+    nb = _lib.w4_expert_sort_workspace_bytes(T, top, E)
+    # one allocation: offsets, place, order, and the workspace behind them
+    slots = T * top
+    buf = torch.empty(E + 1 + 2 * slots + (nb + 3) // 4, dtype=torch.int32, device=device)
+    offsets, place, order, work = buf.split((E + 1, slots, slots, (nb + 3) // 4))
+    return ExpertRows(offsets, place.view(T, top), order), work, nb
+
+
+def _expert_rows(rows, dev):
+    """Checks the ExpertRows of a call: (T, top, E)."""
+    if not isinstance(rows, ExpertRows):
+        raise TypeError("rows must be an ExpertRows")
+    if rows.place.dim() != 2:
+        raise ValueError("rows.place must be [tokens, top]")
+    T, top = rows.place.shape
+    E = _experts(rows.offsets)
+    _ptr(rows.offsets, torch.int32, dev, "rows.offsets")
+    _ptr(rows.place, torch.int32, dev, "rows.place")
+    return T, top, E
+
+
+def expert_sort(experts, E):
+    """Sorts the slots of a router's choice by expert: experts int64 or int32 [T, top] on the GPU, ids outside
+    [0, E) being of no expert (their slots are dropped).  Returns ExpertRows, whose offsets the grouped linears
+    take.  Slots of one expert keep their order."""
+    dev, T, top, size = _ids(experts, E)
+    rows, work, nb = _empty_rows(T, top, E, experts.device)
+    _launch("w4_expert_sort", dev, experts.data_ptr(), size, T, top, E, rows.offsets.data_ptr(), rows.place.data_ptr(),
+            rows.order.data_ptr(), work.data_ptr(), nb)
+    return rows
+
+
+def _take(x, rows, dev, out=None):
+    T, top, E = _expert_rows(rows, dev)
+    if x.shape[0] != T:
+        raise ValueError(f"x must have {T} rows (got {x.shape[0]})")
+    xs = torch.empty((T * top,) + x.shape[1:], dtype=x.dtype, device=x.device) if out is None else out
+    width = x.element_size() * (x.shape[1] if x.dim() == 2 else 1)
+    _launch("w4_expert_take", dev, x.data_ptr(), T, width, top, rows.offsets.data_ptr(), E, rows.place.data_ptr(),
+            _ptr(xs, x.dtype, dev, "out", (T * top,) + x.shape[1:]))
+    return xs
+
+
+def _weights(weights, dev, T, top):
+    """(address, w4_type) of a call's weights; of none."""
+    if weights is None:
+        return None, 1
+    if not isinstance(weights, torch.Tensor) or weights.dtype not in OUT_DTYPES:
+        raise TypeError("weights must be a float32 or bfloat16 torch.Tensor")
+    return _ptr(weights, weights.dtype, dev, "weights", (T, top)), _TYPES[weights.dtype]
+
+
+def _combine(y, weights, rows, dev, out, out_dtype):
+    T, top, E = _expert_rows(rows, dev)
+    if y.shape[0] != T * top:
+        raise ValueError(f"y must have {T * top} rows (got {y.shape[0]})")
+    K = y.shape[1]
+    o, _ = _output(out, out_dtype, T, K, y.device)
+    w, wt = _weights(weights, dev, T, top)
+    _launch("w4_expert_combine", dev, y.data_ptr(), _TYPES[y.dtype], w, wt, T, top, K, rows.place.data_ptr(),
+            _ptr(o, o.dtype, dev, "out", (T, K)), _TYPES[o.dtype])
+    return o
+
+
+def expert_combine_backward(grad, y, weights, rows, need_y=True, need_weights=True):
+    """Gradients of expert_combine for grad [T, K]: (dy [T * top, K] of y's type, zeros in rows of no slot;
+    dweights [T, top] of weights' type, zeros for dropped slots), None where not needed.  (Autograd calls it
+    for an expert_combine whose y or weights require gradients.)"""
+    dev, T, K = _rows(grad, OUT_DTYPES, "grad")
+    _, n, _ = _rows(y, OUT_DTYPES, "y")
+    t, top, E = _expert_rows(rows, dev)
+    if t != T or tuple(y.shape) != (T * top, K):
+        raise ValueError(f"grad must be [{t}, K] and y [{t * top}, K] (got {tuple(grad.shape)} and {tuple(y.shape)})")
+    w, wt = _weights(weights, dev, T, top)
+    dy = torch.empty_like(y) if need_y else None
+    dw = torch.empty_like(weights) if need_weights and weights is not None else None
+    _launch("w4_expert_combine_backward", dev, grad.data_ptr(), _TYPES[grad.dtype], _ptr(y, y.dtype, dev, "y"),
+            _TYPES[y.dtype], w, wt, T, top, K, rows.offsets.data_ptr(), E, rows.place.data_ptr(),
+            None if dy is None else dy.data_ptr(), None if dw is None else dw.data_ptr())
+    return dy, dw
+
+
+class _TakeFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, rows):
+        ctx.rows = rows
+        return _take(x, rows, x.get_device())
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        return _combine(grad.contiguous(), None, ctx.rows, grad.get_device(), None, grad.dtype), None
+
+
+class _DispatchFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, experts, E):
+        xs, rows = _dispatch(x, experts, E)
+        ctx.rows = rows
+        ctx.mark_non_differentiable(*rows)
+        return (xs,) + rows
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad, *_):
+        return _combine(grad.contiguous(), None, ctx.rows, grad.get_device(), None, grad.dtype), None, None
+
+
+class _CombineFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, weights, rows, out_dtype):
+        ctx.save_for_backward(y, weights)
+        ctx.rows = rows
+        return _combine(y, weights, rows, y.get_device(), None, out_dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        y, weights = ctx.saved_tensors
+        return expert_combine_backward(grad.contiguous(), y, weights, ctx.rows, *ctx.needs_input_grad[:2]) + (None, None)
+
+
+def _row_tensor(x, name):
+    if isinstance(x, torch.Tensor) and x.dim() not in (1, 2):
+        raise ValueError(f"{name} must be 1-D or 2-D (got shape {tuple(x.shape)})")
+    return _first(x, _ROW_DTYPES, name)[0]
+
+
+def expert_take(x, rows, out=None):
+    """x [T, K] (or [T]) of bf16, fp32, uint8 or int8 -> its rows in the experts' order, [T * top, K]: row
+    rows.place[t, j] is x[t]; rows of no slot are zeros.  Differentiable (bf16, fp32) without `out`."""
+    dev = _row_tensor(x, "x")
+    if out is None and x.requires_grad and torch.is_grad_enabled():
+        if x.dim() != 2:
+            raise ValueError("x must be 2-D for its gradient")
+        return _TakeFunction.apply(x, rows)
+    return _take(x, rows, dev, out)
+
+
+def _dispatch(x, experts, E):
+    dev, T, top, size = _ids(experts, E)
+    if x.get_device() != dev:
+        raise ValueError(f"experts: tensors on several devices ({experts.device} and {x.device})")
+    if x.shape[0] != T:
+        raise ValueError(f"x must have {T} rows (got {x.shape[0]})")
+    rows, work, nb = _empty_rows(T, top, E, x.device)
+    xs = torch.empty((T * top,) + x.shape[1:], dtype=x.dtype, device=x.device)
+    width = x.element_size() * (x.shape[1] if x.dim() == 2 else 1)
+    _launch("w4_expert_dispatch", dev, x.data_ptr(), width, experts.data_ptr(), size, T, top, E, rows.offsets.data_ptr(),
+            rows.place.data_ptr(), rows.order.data_ptr(), xs.data_ptr(), work.data_ptr(), nb)
+    return xs, rows
+
+
+def expert_dispatch(x, experts, E):
+    """expert_sort(experts, E) and expert_take(x, rows) in one call: (xs, ExpertRows).  Differentiable with
+    respect to x (bf16, fp32)."""
+    _row_tensor(x, "x")
+    if x.requires_grad and torch.is_grad_enabled():
+        if x.dim() != 2:
+            raise ValueError("x must be 2-D for its gradient")
+        xs, *rows = _DispatchFunction.apply(x, experts, E)
+        return xs, ExpertRows(*rows)
+    return _dispatch(x, experts, E)
+
+
+def expert_combine(y, weights, rows, out=None, out_dtype=None):
+    """The experts' rows y [T * top, K] (bf16, or fp32) brought back to their tokens: out [T, K] = sum over j of
+    weights[t, j] * y[rows.place[t, j]], in fp32, of y's type unless `out_dtype` (or `out`) says otherwise.
+    weights fp32 or bf16 [T, top], or None for a plain sum.  Dropped slots add nothing, and rows of no slot are
+    not read.  Differentiable with respect to y and weights without `out`."""
+    dev, _, _ = _rows(y, OUT_DTYPES, "y")
+    dtype = y.dtype if out_dtype is None else out_dtype
+    if out is None and torch.is_grad_enabled() and (
+            y.requires_grad or (isinstance(weights, torch.Tensor) and weights.requires_grad)):
+        return _CombineFunction.apply(y, weights, rows, dtype)
+    return _combine(y, weights, rows, dev, out, dtype)
+
+
+class MX4Linear:
+    """A microscaled 4-bit weight held in native layout, callable on bf16 (or fp32) activations: they are
+    quantized block by block and multiplied in 4 bits."""
+
+    def __init__(self, q, s, N, K):
+        self.q, self.s, self.N, self.K = q, s, N, K
+
+    @classmethod
+    def from_float(cls, W):
+        if not isinstance(W, torch.Tensor) or W.dim() != 2:
+            raise TypeError("W must be a 2-D torch.Tensor")
+        q, s = quantize_mx4(W)
+        return cls(q, s, W.shape[0], W.shape[1])
+
+    def __call__(self, x, out=None, out_dtype=torch.bfloat16):
+        xq, xs = quantize_tokens_mx4(x)
+        return linear_mx4(xq, xs, self.q, self.s, self.N, out=out, out_dtype=out_dtype)
+
+
 class W8Linear:
     """An 8-bit weight held in native layout, callable on bf16 (or fp32) activations: they are
     quantized token by token and multiplied in int8."""
@@ -832,6 +1228,10 @@ __all__ = [
     "W4Linear", "W8Linear", "SplitWorkspace",
     "grouped_linear", "grouped_linear_w8a8", "linear_w8a8", "pack_w8", "packed_bytes_w8", "quantize_rtn_experts",
     "quantize_tokens", "quantize_w8", "unpack_w8",
+    "MX4Linear", "dequantize_mx4", "dequantize_tokens_mx4", "grouped_linear_mx4", "linear_mx4", "pack_mx4",
+    "packed_bytes_mx4", "quantize_mx4", "quantize_tokens_mx4", "scale_bytes_mx4", "unpack_mx4",
+    "ExpertRows", "MAX_EXPERTS", "MAX_SLOTS", "expert_combine", "expert_combine_backward", "expert_dispatch",
+    "expert_sort", "expert_take",
     "awq_scales", "channel_absmean", "library", "linear", "linear_awq", "linear_batched",
     "quantize_rtn_scaled", "scale_activations", "sq_error",
     "pack", "packed_bytes", "quantize_rtn", "scale_count", "unpack",

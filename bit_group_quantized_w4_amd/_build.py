@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libw4.so")
 
 LIB_SOURCES = ["abi.cpp", "quantize.hip", "linear.hip", "awq.hip", "gptq.hip", "dense.hip", "int8.hip",
-               "grouped.hip"]
+               "grouped.hip", "mx4.hip", "experts.hip"]
 
 ARCH = "gfx950"
 

@@ -23,6 +23,7 @@ constexpr int64_t kGroup = 128;
 constexpr int64_t kMaxK = int64_t(1) << 24;       // keeps every in-kernel index in range
 constexpr int64_t kMaxN = (int64_t(1) << 31) - 16;
 constexpr int64_t kMaxM = 65535 * 4;              // kept within 32-bit block indices
+constexpr int64_t kMaxRowBytes = int64_t(1) << 26;  // of a row that is moved as it is: kMaxK fp32 values
 
 bool k_ok(int64_t K) { return K > 0 && K % kGroup == 0 && K <= kMaxK; }
 bool n_ok(int64_t N) { return N >= 0 && N <= kMaxN; }
@@ -267,6 +268,132 @@ w4_status linear_grouped(const uint16_t* x, int64_t M, int64_t K, const int32_t*
       overlaps(y, yb, q, (size_t)experts * qb) || overlaps(y, yb, d, (size_t)experts * db))
     return W4_ERR_ARG;
   return hip_status(w4::launch_linear_grouped(x, M, K, offsets, experts, q, d, s16, N, y, out == 4, stream));
+}
+
+// 4-bit floating point: shapes of an N x K matrix, and of M rows of activations.
+bool mx4_ok(int64_t N, int64_t K) { return n_ok(N) && k8_ok(K); }
+size_t mx4_canon_bytes(int64_t rows, int64_t K) { return (size_t)rows * (size_t)K / 2; }
+size_t mx4_canon_scales(int64_t rows, int64_t K) { return (size_t)rows * (size_t)K / 32; }
+
+w4_status weights_mx4(const void* W, size_t elem, int64_t N, int64_t K, const uint8_t* q, const uint8_t* s) {
+  if (!W || !q || !s) return W4_ERR_NULL;
+  if (!aligned(W, 16) || !aligned(q, 16) || !aligned(s, 16)) return W4_ERR_ALIGN;
+  const size_t qb = w4_mx4_packed_bytes(N, K), sb = w4_mx4_scale_bytes(N, K), wb = elem * (size_t)N * K;
+  if (overlaps(q, qb, s, sb) || overlaps(q, qb, W, wb) || overlaps(s, sb, W, wb)) return W4_ERR_ARG;
+  return W4_OK;
+}
+
+w4_status quantize_mx4(const void* W, size_t elem, int64_t N, int64_t K, uint8_t* q, uint8_t* s, hipStream_t stream) {
+  if (!mx4_ok(N, K)) return W4_ERR_SHAPE;
+  if (N == 0) return W4_OK;
+  if (w4_status e = weights_mx4(W, elem, N, K, q, s)) return e;
+  return hip_status(w4::launch_quantize_mx4(W, elem == 4, N, K, q, s, stream));
+}
+
+w4_status dequantize_mx4(const uint8_t* q, const uint8_t* s, int64_t N, int64_t K, void* W, size_t elem,
+                         hipStream_t stream) {
+  if (!mx4_ok(N, K)) return W4_ERR_SHAPE;
+  if (N == 0) return W4_OK;
+  if (w4_status e = weights_mx4(W, elem, N, K, q, s)) return e;
+  return hip_status(w4::launch_dequantize_mx4(q, s, N, K, W, elem == 4, stream));
+}
+
+w4_status pack_mx4(const uint8_t* canon, const uint8_t* canon_scales, int64_t N, int64_t K, const uint8_t* q,
+                   const uint8_t* s, bool pack, hipStream_t stream) {
+  if (!mx4_ok(N, K)) return W4_ERR_SHAPE;
+  if (N == 0) return W4_OK;
+  if (!canon || !canon_scales || !q || !s) return W4_ERR_NULL;
+  if (!aligned(canon, 16) || !aligned(q, 16) || !aligned(s, 16)) return W4_ERR_ALIGN;
+  const size_t cb = mx4_canon_bytes(N, K), cs = mx4_canon_scales(N, K);
+  const size_t qb = w4_mx4_packed_bytes(N, K), sb = w4_mx4_scale_bytes(N, K);
+  if (overlaps(canon, cb, q, qb) || overlaps(canon, cb, s, sb) || overlaps(canon_scales, cs, q, qb) ||
+      overlaps(canon_scales, cs, s, sb) || overlaps(pack ? q : canon, pack ? qb : cb, pack ? s : canon_scales, pack ? sb : cs))
+    return W4_ERR_ARG;
+  return hip_status(w4::launch_pack_mx4(const_cast<uint8_t*>(canon), const_cast<uint8_t*>(canon_scales), N, K,
+                                        const_cast<uint8_t*>(q), const_cast<uint8_t*>(s), pack, stream));
+}
+
+w4_status tokens_mx4(const void* x, size_t elem, int64_t M, int64_t K, const uint8_t* xq, const uint8_t* xs) {
+  if (M < 0 || M > kMaxM || !k8_ok(K)) return W4_ERR_SHAPE;
+  if (M == 0) return W4_OK;
+  if (!x || !xq || !xs) return W4_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(xq, 16) || !aligned(xs, 4)) return W4_ERR_ALIGN;
+  const size_t qb = mx4_canon_bytes(M, K), sb = mx4_canon_scales(M, K), xb = elem * (size_t)M * K;
+  if (overlaps(xq, qb, xs, sb) || overlaps(xq, qb, x, xb) || overlaps(xs, sb, x, xb)) return W4_ERR_ARG;
+  return W4_OK;
+}
+
+w4_status quantize_tokens_mx4(const void* x, size_t elem, int64_t M, int64_t K, uint8_t* xq, uint8_t* xs,
+                              hipStream_t stream) {
+  if (w4_status e = tokens_mx4(x, elem, M, K, xq, xs)) return e;
+  return M == 0 ? W4_OK : hip_status(w4::launch_quantize_tokens_mx4(x, elem == 4, M, K, xq, xs, stream));
+}
+
+w4_status dequantize_tokens_mx4(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, void* x, size_t elem,
+                                hipStream_t stream) {
+  if (w4_status e = tokens_mx4(x, elem, M, K, xq, xs)) return e;
+  return M == 0 ? W4_OK : hip_status(w4::launch_dequantize_tokens_mx4(xq, xs, M, K, x, elem == 4, stream));
+}
+
+w4_status linear_mx4(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, bool grouped, const int32_t* offsets,
+                     int64_t experts, const uint8_t* q, const uint8_t* s, int64_t N, void* y, size_t out,
+                     hipStream_t stream) {
+  if (M < 0 || M > kMaxM || !mx4_ok(N, K) || experts < 0 || experts > W4_MAX_EXPERTS) return W4_ERR_SHAPE;
+  if (M == 0 || N == 0 || experts == 0) return W4_OK;
+  const size_t qb = w4_mx4_packed_bytes(N, K), sb = w4_mx4_scale_bytes(N, K);
+  if (qb >= (size_t)1 << 31) return W4_ERR_SHAPE;  // one matrix is addressed with 32-bit offsets
+  if (!w4::fits_linear_mx4(M, N, experts, grouped)) return W4_ERR_SHAPE;
+  if (!xq || !xs || !q || !s || !y || (grouped && !offsets)) return W4_ERR_NULL;
+  if (!aligned(xq, 16) || !aligned(xs, 4) || !aligned(q, 16) || !aligned(s, 16) || !aligned(y, out) ||
+      !aligned(offsets, 4))
+    return W4_ERR_ALIGN;
+  const size_t yb = out * (size_t)M * N;
+  if (overlaps(y, yb, xq, mx4_canon_bytes(M, K)) || overlaps(y, yb, xs, mx4_canon_scales(M, K)) ||
+      overlaps(y, yb, q, (size_t)experts * qb) || overlaps(y, yb, s, (size_t)experts * sb) ||
+      (grouped && overlaps(y, yb, offsets, 4 * ((size_t)experts + 1))))
+    return W4_ERR_ARG;
+  return hip_status(w4::launch_linear_mx4(xq, xs, M, K, grouped ? offsets : nullptr, experts, q, s, N, y, out == 4,
+                                          stream));
+}
+
+// The way to the experts and back: slots of a call, at most as many as rows of a product.
+bool slots_ok(int64_t tokens, int64_t top) {
+  return tokens >= 0 && tokens <= kMaxM && top >= 1 && top <= kMaxM && tokens * top <= kMaxM;
+}
+bool experts_ok(int64_t experts) { return experts >= 0 && experts <= W4_MAX_EXPERTS; }
+bool type_ok(int type) { return type == W4_BF16 || type == W4_F32; }
+size_t type_bytes(int type) { return type == W4_F32 ? 4 : 2; }
+
+// Whether any output of a call overlaps another output or an input (nullptr: not there).
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+bool any_overlap(const Span* out, int outs, const Span* in, int ins) {
+  for (int i = 0; i < outs; ++i) {
+    if (!out[i].at) continue;
+    for (int j = 0; j < i; ++j)
+      if (out[j].at && overlaps(out[i].at, out[i].bytes, out[j].at, out[j].bytes)) return true;
+    for (int j = 0; j < ins; ++j)
+      if (in[j].at && overlaps(out[i].at, out[i].bytes, in[j].at, in[j].bytes)) return true;
+  }
+  return false;
+}
+
+w4_status check_sort(const void* experts, int id_bytes, int64_t tokens, int64_t top, int64_t count, int32_t* offsets,
+                     int32_t* place, int32_t* order, void* workspace, size_t workspace_bytes) {
+  if (!slots_ok(tokens, top) || !experts_ok(count)) return W4_ERR_SHAPE;
+  if (id_bytes != 4 && id_bytes != 8) return W4_ERR_ARG;
+  const int64_t slots = tokens * top;
+  if (!offsets || (slots && (!experts || !place || !order)) || !workspace) return W4_ERR_NULL;
+  if (!aligned(experts, id_bytes) || !aligned(offsets, 4) || !aligned(place, 4) || !aligned(order, 4) ||
+      !aligned(workspace, 4))
+    return W4_ERR_ALIGN;
+  if (workspace_bytes < w4_expert_sort_workspace_bytes(tokens, top, count)) return W4_ERR_ARG;
+  const Span out[] = {{offsets, 4 * ((size_t)count + 1)}, {place, 4 * (size_t)slots}, {order, 4 * (size_t)slots},
+                      {workspace, workspace_bytes}};
+  const Span in[] = {{experts, (size_t)id_bytes * slots}};
+  return any_overlap(out, 4, in, 1) ? W4_ERR_ARG : W4_OK;
 }
 
 }  // namespace
@@ -992,6 +1119,178 @@ w4_status w4_linear_grouped_f32_s16(const uint16_t* x, int64_t M, int64_t K, con
                                     const uint8_t* q_packed, const uint16_t* d_packed, int64_t N, float* y,
                                     hipStream_t stream) {
   return linear_grouped(x, M, K, offsets, experts, q_packed, d_packed, true, N, y, 4, stream);
+}
+
+// ---------------------------------------------------------------------------
+// microscaled 4-bit floating point
+// ---------------------------------------------------------------------------
+size_t w4_mx4_packed_bytes(int64_t N, int64_t K) {
+  if (!mx4_ok(N, K)) return 0;
+  return (size_t)padded_rows(N) * (size_t)((K + 255) / 256 * 128);
+}
+
+size_t w4_mx4_scale_bytes(int64_t N, int64_t K) {
+  if (!mx4_ok(N, K)) return 0;
+  return (size_t)padded_rows(N) * (size_t)((K + 511) / 512 * 16);
+}
+
+w4_status w4_quantize_mx4(const uint16_t* W, int64_t N, int64_t K, uint8_t* q_packed, uint8_t* s_packed,
+                          hipStream_t stream) {
+  return quantize_mx4(W, 2, N, K, q_packed, s_packed, stream);
+}
+
+w4_status w4_quantize_mx4_f32(const float* W, int64_t N, int64_t K, uint8_t* q_packed, uint8_t* s_packed,
+                              hipStream_t stream) {
+  return quantize_mx4(W, 4, N, K, q_packed, s_packed, stream);
+}
+
+w4_status w4_dequantize_mx4(const uint8_t* q_packed, const uint8_t* s_packed, int64_t N, int64_t K, uint16_t* W,
+                            hipStream_t stream) {
+  return dequantize_mx4(q_packed, s_packed, N, K, W, 2, stream);
+}
+
+w4_status w4_dequantize_mx4_f32(const uint8_t* q_packed, const uint8_t* s_packed, int64_t N, int64_t K, float* W,
+                                hipStream_t stream) {
+  return dequantize_mx4(q_packed, s_packed, N, K, W, 4, stream);
+}
+
+w4_status w4_pack_mx4(const uint8_t* q_canon, const uint8_t* s_canon, int64_t N, int64_t K, uint8_t* q_packed,
+                      uint8_t* s_packed, hipStream_t stream) {
+  return pack_mx4(q_canon, s_canon, N, K, q_packed, s_packed, true, stream);
+}
+
+w4_status w4_unpack_mx4(const uint8_t* q_packed, const uint8_t* s_packed, int64_t N, int64_t K, uint8_t* q_canon,
+                        uint8_t* s_canon, hipStream_t stream) {
+  return pack_mx4(q_canon, s_canon, N, K, q_packed, s_packed, false, stream);
+}
+
+w4_status w4_quantize_tokens_mx4(const uint16_t* x, int64_t M, int64_t K, uint8_t* xq, uint8_t* xs, hipStream_t stream) {
+  return quantize_tokens_mx4(x, 2, M, K, xq, xs, stream);
+}
+
+w4_status w4_quantize_tokens_mx4_f32(const float* x, int64_t M, int64_t K, uint8_t* xq, uint8_t* xs, hipStream_t stream) {
+  return quantize_tokens_mx4(x, 4, M, K, xq, xs, stream);
+}
+
+w4_status w4_dequantize_tokens_mx4(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, uint16_t* x,
+                                   hipStream_t stream) {
+  return dequantize_tokens_mx4(xq, xs, M, K, x, 2, stream);
+}
+
+w4_status w4_dequantize_tokens_mx4_f32(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, float* x,
+                                       hipStream_t stream) {
+  return dequantize_tokens_mx4(xq, xs, M, K, x, 4, stream);
+}
+
+w4_status w4_linear_mx4(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, const uint8_t* q_packed,
+                        const uint8_t* s_packed, int64_t N, uint16_t* y, hipStream_t stream) {
+  return linear_mx4(xq, xs, M, K, false, nullptr, 1, q_packed, s_packed, N, y, 2, stream);
+}
+
+w4_status w4_linear_mx4_f32(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, const uint8_t* q_packed,
+                            const uint8_t* s_packed, int64_t N, float* y, hipStream_t stream) {
+  return linear_mx4(xq, xs, M, K, false, nullptr, 1, q_packed, s_packed, N, y, 4, stream);
+}
+
+w4_status w4_linear_grouped_mx4(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, const int32_t* offsets,
+                                int64_t experts, const uint8_t* q_packed, const uint8_t* s_packed, int64_t N, uint16_t* y,
+                                hipStream_t stream) {
+  return linear_mx4(xq, xs, M, K, true, offsets, experts, q_packed, s_packed, N, y, 2, stream);
+}
+
+w4_status w4_linear_grouped_mx4_f32(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, const int32_t* offsets,
+                                    int64_t experts, const uint8_t* q_packed, const uint8_t* s_packed, int64_t N, float* y,
+                                    hipStream_t stream) {
+  return linear_mx4(xq, xs, M, K, true, offsets, experts, q_packed, s_packed, N, y, 4, stream);
+}
+
+// ---------------------------------------------------------------------------
+// rows to the experts and back
+// ---------------------------------------------------------------------------
+size_t w4_expert_sort_workspace_bytes(int64_t tokens, int64_t top, int64_t experts) {
+  if (!slots_ok(tokens, top) || !experts_ok(experts)) return 0;
+  return w4::expert_sort_workspace(tokens * top, experts);
+}
+
+w4_status w4_expert_sort(const void* ids, int id_bytes, int64_t tokens, int64_t top, int64_t experts, int32_t* offsets,
+                         int32_t* place, int32_t* order, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (w4_status e = check_sort(ids, id_bytes, tokens, top, experts, offsets, place, order, workspace, workspace_bytes))
+    return e;
+  return hip_status(w4::launch_expert_sort(ids, id_bytes == 8, tokens * top, experts, offsets, place, order, workspace,
+                                           stream));
+}
+
+w4_status w4_expert_take(const void* x, int64_t tokens, int64_t row_bytes, int64_t top, const int32_t* offsets,
+                         int64_t experts, const int32_t* place, void* xs, hipStream_t stream) {
+  if (!slots_ok(tokens, top) || !experts_ok(experts) || row_bytes < 0 || row_bytes > kMaxRowBytes) return W4_ERR_SHAPE;
+  if (tokens == 0 || row_bytes == 0) return W4_OK;
+  if (!x || !offsets || !place || !xs) return W4_ERR_NULL;
+  if (!aligned(offsets, 4) || !aligned(place, 4)) return W4_ERR_ALIGN;
+  const size_t slots = (size_t)(tokens * top);
+  const Span out[] = {{xs, slots * row_bytes}};
+  const Span in[] = {{x, (size_t)tokens * row_bytes}, {offsets, 4 * ((size_t)experts + 1)}, {place, 4 * slots}};
+  if (any_overlap(out, 1, in, 3)) return W4_ERR_ARG;
+  return hip_status(w4::launch_expert_take(x, tokens, row_bytes, top, offsets, experts, place, xs, stream));
+}
+
+w4_status w4_expert_dispatch(const void* x, int64_t row_bytes, const void* ids, int id_bytes, int64_t tokens, int64_t top,
+                             int64_t experts, int32_t* offsets, int32_t* place, int32_t* order, void* xs, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream) {
+  if (row_bytes < 0 || row_bytes > kMaxRowBytes) return W4_ERR_SHAPE;
+  if (w4_status e = check_sort(ids, id_bytes, tokens, top, experts, offsets, place, order, workspace, workspace_bytes))
+    return e;
+  if (tokens && row_bytes) {
+    if (!x || !xs) return W4_ERR_NULL;
+    const size_t slots = (size_t)(tokens * top);
+    const Span out[] = {{offsets, 4 * ((size_t)experts + 1)}, {place, 4 * slots}, {order, 4 * slots},
+                        {workspace, workspace_bytes}, {xs, slots * row_bytes}};
+    const Span in[] = {{x, (size_t)tokens * row_bytes}, {ids, (size_t)id_bytes * slots}};
+    if (any_overlap(out, 5, in, 2)) return W4_ERR_ARG;
+  }
+  if (w4_status e = hip_status(w4::launch_expert_sort(ids, id_bytes == 8, tokens * top, experts, offsets, place, order,
+                                                      workspace, stream)))
+    return e;
+  if (tokens == 0 || row_bytes == 0) return W4_OK;
+  return hip_status(w4::launch_expert_take(x, tokens, row_bytes, top, offsets, experts, place, xs, stream));
+}
+
+w4_status w4_expert_combine(const void* y, int y_type, const void* weights, int weights_type, int64_t tokens, int64_t top,
+                            int64_t K, const int32_t* place, void* out, int out_type, hipStream_t stream) {
+  if (!slots_ok(tokens, top) || K < 0 || K > kMaxK) return W4_ERR_SHAPE;
+  if (!type_ok(y_type) || !type_ok(weights_type) || !type_ok(out_type)) return W4_ERR_ARG;
+  if (tokens == 0 || K == 0) return W4_OK;
+  if (!y || !place || !out) return W4_ERR_NULL;
+  if (!aligned(y, type_bytes(y_type)) || !aligned(weights, type_bytes(weights_type)) || !aligned(place, 4) ||
+      !aligned(out, type_bytes(out_type)))
+    return W4_ERR_ALIGN;
+  const size_t slots = (size_t)(tokens * top);
+  const Span to[] = {{out, type_bytes(out_type) * (size_t)tokens * K}};
+  const Span in[] = {{y, type_bytes(y_type) * slots * K}, {weights, type_bytes(weights_type) * slots}, {place, 4 * slots}};
+  if (any_overlap(to, 1, in, 3)) return W4_ERR_ARG;
+  const w4::CombineArgs a{y, weights, place, out, K, (int)slots, (int)top, y_type == W4_F32, weights_type == W4_F32,
+                          out_type == W4_F32};
+  return hip_status(w4::launch_expert_combine(a, stream));
+}
+
+w4_status w4_expert_combine_backward(const void* dout, int out_type, const void* y, int y_type, const void* weights,
+                                     int weights_type, int64_t tokens, int64_t top, int64_t K, const int32_t* offsets,
+                                     int64_t experts, const int32_t* place, void* dy, void* dweights, hipStream_t stream) {
+  if (!slots_ok(tokens, top) || !experts_ok(experts) || K < 0 || K > kMaxK) return W4_ERR_SHAPE;
+  if (!type_ok(y_type) || !type_ok(weights_type) || !type_ok(out_type)) return W4_ERR_ARG;
+  if (tokens == 0 || (!dy && !dweights)) return W4_OK;
+  if ((K && (!dout || (dweights && !y))) || !place || (dy && !offsets)) return W4_ERR_NULL;
+  if (!aligned(dout, type_bytes(out_type)) || !aligned(y, type_bytes(y_type)) || !aligned(dy, type_bytes(y_type)) ||
+      !aligned(weights, type_bytes(weights_type)) || !aligned(dweights, type_bytes(weights_type)) || !aligned(place, 4) ||
+      !aligned(offsets, 4))
+    return W4_ERR_ALIGN;
+  const size_t slots = (size_t)(tokens * top);
+  const Span out[] = {{dy, type_bytes(y_type) * slots * K}, {dweights, type_bytes(weights_type) * slots}};
+  const Span in[] = {{dout, type_bytes(out_type) * (size_t)tokens * K}, {y, type_bytes(y_type) * slots * K},
+                     {weights, type_bytes(weights_type) * slots}, {place, 4 * slots}, {offsets, 4 * ((size_t)experts + 1)}};
+  if (any_overlap(out, 2, in, 5)) return W4_ERR_ARG;
+  const w4::CombineBackwardArgs a{dout, y, weights, place, offsets ? offsets + experts : nullptr, dy, dweights, K,
+                                  (int)slots, (int)top, y_type == W4_F32, weights_type == W4_F32, out_type == W4_F32};
+  return hip_status(w4::launch_expert_combine_backward(a, stream));
 }
 
 }  // extern "C"

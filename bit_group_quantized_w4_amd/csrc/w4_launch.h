@@ -180,4 +180,54 @@ hipError_t launch_linear_grouped(const uint16_t* x, int64_t M, int64_t K, const 
                                  const uint8_t* q, const void* d, bool s16, int64_t N, void* y, bool f32,
                                  hipStream_t stream);
 
+// Microscaled 4-bit floating point (mx4.hip).
+hipError_t launch_quantize_mx4(const void* W, bool f32, int64_t N, int64_t K, uint8_t* q, uint8_t* s, hipStream_t stream);
+hipError_t launch_dequantize_mx4(const uint8_t* q, const uint8_t* s, int64_t N, int64_t K, void* W, bool f32,
+                                 hipStream_t stream);
+// Row-major codes [N][K / 2] and scales [N][K / 32] -> native (pack) or back.
+hipError_t launch_pack_mx4(uint8_t* canon, uint8_t* canon_scales, int64_t N, int64_t K, uint8_t* q, uint8_t* s, bool pack,
+                           hipStream_t stream);
+hipError_t launch_quantize_tokens_mx4(const void* x, bool f32, int64_t M, int64_t K, uint8_t* xq, uint8_t* xs,
+                                      hipStream_t stream);
+hipError_t launch_dequantize_tokens_mx4(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, void* x, bool f32,
+                                        hipStream_t stream);
+// y = x^ w^T; offsets as for launch_linear_w8a8.
+bool fits_linear_mx4(int64_t M, int64_t N, int64_t experts, bool grouped);  // the tiles fit a launch
+hipError_t launch_linear_mx4(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, const int32_t* offsets,
+                             int64_t experts, const uint8_t* q, const uint8_t* s, int64_t N, void* y, bool f32,
+                             hipStream_t stream);
+
+// Rows to the experts and back (experts.hip).  slots = tokens * top.
+size_t expert_sort_workspace(int64_t slots, int64_t experts);
+// ids int64 (wide) or int32 [slots].
+hipError_t launch_expert_sort(const void* ids, bool wide, int64_t slots, int64_t experts, int32_t* offsets, int32_t* place,
+                              int32_t* order, void* workspace, hipStream_t stream);
+// Rows of `bytes` bytes: xs[place[t][j]] = x[t], zeros from row offsets[experts] on.
+hipError_t launch_expert_take(const void* x, int64_t tokens, int64_t bytes, int64_t top, const int32_t* offsets,
+                              int64_t experts, const int32_t* place, void* xs, hipStream_t stream);
+
+struct CombineArgs {
+  const void* y;       // [slots][K]
+  const void* w;       // [slots], or nullptr: ones
+  const int32_t* place;
+  void* out;           // [slots / top][K]
+  int64_t K;
+  int slots, top;
+  bool y_f32, w_f32, out_f32;  // fp32, else bf16
+};
+struct CombineBackwardArgs {
+  const void* dout;    // [slots / top][K], of out's type
+  const void* y;       // [slots][K]; read for dw only
+  const void* w;       // [slots], or nullptr: ones
+  const int32_t* place;
+  const int32_t* valid_at;  // the number of rows that slots have (offsets[experts])
+  void* dy;            // [slots][K] of y's type, or nullptr
+  void* dw;            // [slots] of w's type, or nullptr
+  int64_t K;
+  int slots, top;
+  bool y_f32, w_f32, out_f32;
+};
+hipError_t launch_expert_combine(const CombineArgs& a, hipStream_t stream);
+hipError_t launch_expert_combine_backward(const CombineBackwardArgs& a, hipStream_t stream);
+
 }  // namespace w4

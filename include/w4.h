@@ -714,6 +714,169 @@ w4_status w4_linear_grouped_w8a8_f32(const int8_t* xq, const float* sx, int64_t 
                                      int64_t experts, const int8_t* q_packed, const float* d, int64_t N, float* y,
                                      hipStream_t stream);
 
+/*
+ * Microscaled 4-bit floating point (OCP Microscaling Formats v1.0, MXFP4): codes
+ * that the matrix units multiply as they are, at twice the rate of 8-bit
+ * integers, for weights and for activations.
+ *
+ *   A block is 32 consecutive inputs of a row.  It has one scale, a byte s that
+ *   stands for 2^(s - 127) (E8M0), and 32 codes of four bits: a sign (bit 3) and
+ *   a magnitude 0, 0.5, 1, 1.5, 2, 3, 4 or 6 (E2M1, codes 0 .. 7).
+ *   s     = max(floor(log2(max|v|)) - 2, -127) + 127 over the block (0 for a block
+ *           of zeros); a NaN or infinity in the block gives s = 255 (NaN) and
+ *           codes 0.
+ *   code  = the E2M1 nearest to v / 2^(s - 127), ties to the even code; magnitudes
+ *           above 6 become 6.  The sign of zero is kept.
+ *   Codes and scales have exactly one correct value.  The value of a code under a
+ *   scale is exact in bf16 and fp32 unless it overflows (scales above 252 with the
+ *   largest codes; no quantizer here gives those).
+ *
+ *   y[m][n] = sum_k x^[m][k] w^[n][k] over the values x^, w^ of the codes, products
+ *   exact, accumulated in fp32, rounded to bf16 (nearest even) or stored as fp32.
+ *   Accuracy: the fp32 value lies within
+ *             (K / 128 + 8) * 2^-22 * sum_k |x^[m][k] w^[n][k]|  + K * 2^-120
+ *             of the exact y: one unit in the 22nd bit for each 128 products that the
+ *             matrix unit adds to a sum (2^-23.4 is the most measured) and for each
+ *             sum of a part of K.  The last term covers products and sums below the
+ *             normal range of fp32, which may be taken as zero.
+ *   This holds while no sum overflows fp32.  A NaN scale (255) makes its row of x
+ *   (or of w) give NaN; other rows are unaffected.
+ *   The order in which K is summed depends on the kernel, which is chosen by M, N, K
+ *   and experts; calls of one shape give the same bits.
+ *
+ * ROW-MAJOR LAYOUT (activations, and weights for exchange): codes uint8
+ *   [rows][K / 2], input k in the low (even k) or high (odd k) four bits of byte
+ *   k / 2; scales uint8 [rows][K / 32].
+ *
+ * NATIVE LAYOUT of the weights: rows are padded to a multiple of 16, inputs to one of
+ *   256 (codes) and 512 (scales), with zeros.  Row block r (16 rows), inputs
+ *   256 p .. + 255 are two tiles of 1024 bytes at ((r * P + p) * 2 + t) * 1024, t = 0,
+ *   1, P = ceil(K / 256).  Lane L (0 .. 63) of tile t, 16 bytes, holds row
+ *   16 r + L % 16, inputs 256 p + 64 (L / 16) + 32 t .. + 31 in order.
+ *   The scales of row block r, inputs 512 c .. + 511 are 256 bytes at
+ *   (r * C + c) * 256, C = ceil(K / 512).  The four bytes 4 L .. of lane L hold the
+ *   scales of its row's inputs 512 c + 64 (L / 16) + (0, 32, 256, 288) .. + 31.
+ *
+ * K is a positive multiple of 128, at most 130944, in all of them.
+ */
+
+/* Bytes of native codes, roundup(N, 16) * roundup(K, 256) / 2, and of native scales,
+ * roundup(N, 16) * roundup(K, 512) / 32 (0 on a bad shape). */
+size_t w4_mx4_packed_bytes(int64_t N, int64_t K);
+size_t w4_mx4_scale_bytes(int64_t N, int64_t K);
+
+/* W bf16 (fp32 for _f32) [N][K] -> q_packed (w4_mx4_packed_bytes(N, K) bytes) and
+ * s_packed (w4_mx4_scale_bytes(N, K) bytes), native layout; all 16-byte aligned and
+ * disjoint.  N == 0 does nothing. */
+w4_status w4_quantize_mx4(const uint16_t* W, int64_t N, int64_t K, uint8_t* q_packed, uint8_t* s_packed,
+                          hipStream_t stream);
+w4_status w4_quantize_mx4_f32(const float* W, int64_t N, int64_t K, uint8_t* q_packed, uint8_t* s_packed,
+                              hipStream_t stream);
+
+/* The values of native codes, bf16 (fp32 for _f32) [N][K]; arguments as above. */
+w4_status w4_dequantize_mx4(const uint8_t* q_packed, const uint8_t* s_packed, int64_t N, int64_t K, uint16_t* W,
+                            hipStream_t stream);
+w4_status w4_dequantize_mx4_f32(const uint8_t* q_packed, const uint8_t* s_packed, int64_t N, int64_t K, float* W,
+                                hipStream_t stream);
+
+/* Row-major codes q_canon [N][K / 2] (16-byte aligned) and scales s_canon [N][K / 32]
+ * <-> native layout (16-byte aligned); all disjoint.  Any bytes are codes and scales. */
+w4_status w4_pack_mx4(const uint8_t* q_canon, const uint8_t* s_canon, int64_t N, int64_t K, uint8_t* q_packed,
+                      uint8_t* s_packed, hipStream_t stream);
+w4_status w4_unpack_mx4(const uint8_t* q_packed, const uint8_t* s_packed, int64_t N, int64_t K, uint8_t* q_canon,
+                        uint8_t* s_canon, hipStream_t stream);
+
+/* x bf16 (fp32 for _f32) [M][K] -> row-major xq [M][K / 2] and xs [M][K / 32], and the
+ * values of such codes; x and xq 16-byte, xs 4-byte aligned, disjoint.
+ * 0 <= M <= 262140 (M == 0: nothing is done). */
+w4_status w4_quantize_tokens_mx4(const uint16_t* x, int64_t M, int64_t K, uint8_t* xq, uint8_t* xs, hipStream_t stream);
+w4_status w4_quantize_tokens_mx4_f32(const float* x, int64_t M, int64_t K, uint8_t* xq, uint8_t* xs, hipStream_t stream);
+w4_status w4_dequantize_tokens_mx4(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, uint16_t* x,
+                                   hipStream_t stream);
+w4_status w4_dequantize_tokens_mx4_f32(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, float* x,
+                                       hipStream_t stream);
+
+/* The product above.  xq [M][K / 2] 16-byte and xs [M][K / 32] 4-byte aligned, row-major;
+ * native weights 16-byte aligned; y bf16 [M][N] (2-byte aligned; fp32, 4-byte aligned,
+ * for _f32), overlapping no input (W4_ERR_ARG).  0 <= M <= 262140;
+ * w4_mx4_packed_bytes(N, K) < 2 GiB (else W4_ERR_SHAPE).  M == 0 or N == 0 does
+ * nothing. */
+w4_status w4_linear_mx4(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, const uint8_t* q_packed,
+                        const uint8_t* s_packed, int64_t N, uint16_t* y, hipStream_t stream);
+w4_status w4_linear_mx4_f32(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, const uint8_t* q_packed,
+                            const uint8_t* s_packed, int64_t N, float* y, hipStream_t stream);
+
+/* The product with rows sorted by expert: offsets, experts, launches and rows of no expert
+ * as for w4_linear_grouped_w8a8; expert e's codes at q_packed + e *
+ * w4_mx4_packed_bytes(N, K), its scales at s_packed + e * w4_mx4_scale_bytes(N, K). */
+w4_status w4_linear_grouped_mx4(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, const int32_t* offsets,
+                                int64_t experts, const uint8_t* q_packed, const uint8_t* s_packed, int64_t N, uint16_t* y,
+                                hipStream_t stream);
+w4_status w4_linear_grouped_mx4_f32(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, const int32_t* offsets,
+                                    int64_t experts, const uint8_t* q_packed, const uint8_t* s_packed, int64_t N, float* y,
+                                    hipStream_t stream);
+
+/*
+ * Rows to the experts and back: what stands between a router and the linears grouped
+ * by expert.  A slot is one of a token's `top` choices; slot t * top + j is token t's
+ * j-th.  Slots sorted by expert are the rows that those linears take.
+ *   tokens, top  tokens >= 0, top >= 1, tokens * top <= 262140 (W4_ERR_SHAPE).
+ *   experts      0 <= experts <= W4_MAX_EXPERTS.
+ *   ids      [in]  the experts of the slots, [tokens][top], int32 (id_bytes 4) or int64
+ *                  (id_bytes 8).  An id outside [0, experts) is of no expert: its slot
+ *                  is dropped.  A token may name an expert more than once.
+ *   offsets  [out] int32 [experts + 1]: expert e has rows offsets[e] .. offsets[e+1]-1;
+ *                  offsets[experts] is the number of rows in all.
+ *   place    [out] int32 [tokens][top]: the row of each slot, -1 for a dropped one.
+ *                  Slots of one expert keep their order.
+ *   order    [out] int32 [tokens * top]: the slot of each row, -1 from row
+ *                  offsets[experts] on.
+ *   workspace      device memory of w4_expert_sort_workspace_bytes(tokens, top, experts)
+ *                  bytes, 4-byte aligned; overwritten, of no meaning between calls.
+ *                  Calls that overlap in time need one each.
+ * Index buffers are 4-byte aligned (ids by id_bytes).  Rows may start anywhere that
+ * their type may (row_bytes: anywhere).  Outputs overlap no
+ * input and no other output (W4_ERR_ARG).  The calls below take offsets and place as
+ * w4_expert_sort writes them; other contents give wrong rows, never an access outside
+ * the buffers.
+ */
+
+/* Types of values, for the calls that take several. */
+typedef enum { W4_BF16 = 0, W4_F32 = 1 } w4_type;
+
+size_t w4_expert_sort_workspace_bytes(int64_t tokens, int64_t top, int64_t experts);
+w4_status w4_expert_sort(const void* ids, int id_bytes, int64_t tokens, int64_t top, int64_t experts, int32_t* offsets,
+                         int32_t* place, int32_t* order, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* xs[place[t][j]] = x[t]: rows of row_bytes bytes (0 .. 2^26) of any type, x [tokens], xs
+ * [tokens * top].  Rows of xs from offsets[experts] on become zeros.  Its gradient is
+ * w4_expert_combine without weights. */
+w4_status w4_expert_take(const void* x, int64_t tokens, int64_t row_bytes, int64_t top, const int32_t* offsets,
+                         int64_t experts, const int32_t* place, void* xs, hipStream_t stream);
+
+/* w4_expert_sort and w4_expert_take in one call. */
+w4_status w4_expert_dispatch(const void* x, int64_t row_bytes, const void* ids, int id_bytes, int64_t tokens, int64_t top,
+                             int64_t experts, int32_t* offsets, int32_t* place, int32_t* order, void* xs, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+
+/* out[t] = sum_j weights[t][j] * y[place[t][j]] over the slots that have a row, in fp32 and
+ * in order of j, rounded once to out's type: within (top + 1) * 2^-24 of
+ * sum |weights y|, and that rounding.  Rows that no slot has are not read.
+ *   y [tokens * top][K], weights [tokens][top] (NULL: ones), out [tokens][K], each
+ *   W4_BF16 or W4_F32; 0 <= K <= 2^24. */
+w4_status w4_expert_combine(const void* y, int y_type, const void* weights, int weights_type, int64_t tokens, int64_t top,
+                            int64_t K, const int32_t* place, void* out, int out_type, hipStream_t stream);
+
+/* The gradients of w4_expert_combine for dout (of out's type):
+ *   dy[place[t][j]] = weights[t][j] * dout[t], of y's type; rows that no slot has
+ *                     become zeros (NULL: not computed);
+ *   dweights[t][j]  = sum_k dout[t][k] * y[place[t][j]][k] in fp32, within
+ *                     (K / 64 + 16) * 2^-24 of sum_k |dout y|, rounded to weights' type; 0
+ *                     for a dropped slot (NULL: not computed, and y may be NULL). */
+w4_status w4_expert_combine_backward(const void* dout, int out_type, const void* y, int y_type, const void* weights,
+                                     int weights_type, int64_t tokens, int64_t top, int64_t K, const int32_t* offsets,
+                                     int64_t experts, const int32_t* place, void* dy, void* dweights, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

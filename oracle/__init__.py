@@ -36,8 +36,13 @@ What it computes (sources are the public pages this project is built from):
   with a row as the group and 8-bit codes, the int8 product with token and
   channel scales, and the native layout of 8-bit weights.
 
+* ``mx4_quantize_ref``, ``mx4_linear_ref`` and ``pack_mx4_ref`` -- microscaled 4-bit
+  floating point (OCP MX), its product and the native layout of its weights;
+  ``expert_sort_ref``, ``expert_take_ref`` and ``expert_combine_ref`` with its
+  gradients -- rows sorted by expert and brought back.
+
 Every function here is pinned by ``tests/test_oracle.py`` (the 8-bit ones by
-``tests/test_int8_grouped.py``) against exact
+``tests/test_int8_grouped.py``, the last group by ``tests/test_mx4_experts.py``) against exact
 rational arithmetic, brute force on small inputs, closed forms and hand-derived
 fixtures in ``tests/golden/``; none is "parity unpinned".
 """
@@ -45,9 +50,12 @@ fixtures in ``tests/golden/``; none is "parity unpinned".
 from .awq import (ALPHAS, awq_output_error_ref, awq_search_ref, candidate_scales_ref, channel_absmean_ref,
                   quantize_scaled_ref, scale_activations_ref)
 from .bf16 import bf16_bits_to_f64, f32_to_bf16_bits
+from .experts import expert_combine_backward_ref, expert_combine_ref, expert_sort_ref, expert_take_ref
 from .gptq import gptq_factor_ref, gptq_hessian_ref, gptq_quantize_ref, gptq_ref, output_error_ref
 from .int8 import QMAX8, W8A8_REL, pack_w8_ref, rtn_rows_ref, w8a8_linear_ref
 from .linear import dequantize_ref, offset_scale_ref, w4_linear_ref
+from .mx4 import (E2M1, MX_BLOCK, mx4_bytes_ref, mx4_linear_ref, mx4_quantize_ref, mx4_tolerance, mx4_values_ref,
+                  pack_mx4_ref)
 from .packing import pack_canonical, unpack_canonical
 from .rtn import GROUP, NAN_BITS, QMAX, QMIN, rtn_quantize_ref
 from .tolerance import ABS_TOL, OFFSET_TOL, REL_TOL, admissible, rounding_interval, worst_ratio
@@ -55,7 +63,9 @@ from .tolerance import ABS_TOL, OFFSET_TOL, REL_TOL, admissible, rounding_interv
 __all__ = [
     "ABS_TOL",
     "ALPHAS",
+    "E2M1",
     "GROUP",
+    "MX_BLOCK",
     "NAN_BITS",
     "OFFSET_TOL",
     "QMAX",
@@ -72,14 +82,24 @@ __all__ = [
     "scale_activations_ref",
     "bf16_bits_to_f64",
     "dequantize_ref",
+    "expert_combine_backward_ref",
+    "expert_combine_ref",
+    "expert_sort_ref",
+    "expert_take_ref",
     "f32_to_bf16_bits",
     "gptq_factor_ref",
     "gptq_hessian_ref",
     "gptq_quantize_ref",
     "gptq_ref",
+    "mx4_bytes_ref",
+    "mx4_linear_ref",
+    "mx4_quantize_ref",
+    "mx4_tolerance",
+    "mx4_values_ref",
     "offset_scale_ref",
     "output_error_ref",
     "pack_canonical",
+    "pack_mx4_ref",
     "pack_w8_ref",
     "rounding_interval",
     "rtn_rows_ref",
