@@ -342,7 +342,7 @@ w4_status linear_mx4(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K,
   if (M == 0 || N == 0 || experts == 0) return W4_OK;
   const size_t qb = w4_mx4_packed_bytes(N, K), sb = w4_mx4_scale_bytes(N, K);
   if (qb >= (size_t)1 << 31) return W4_ERR_SHAPE;  // one matrix is addressed with 32-bit offsets
-  if (!w4::fits_linear_mx4(M, N, experts, grouped)) return W4_ERR_SHAPE;
+  if (!w4::fits_linear_mx4(M, N, K, experts, grouped)) return W4_ERR_SHAPE;
   if (!xq || !xs || !q || !s || !y || (grouped && !offsets)) return W4_ERR_NULL;
   if (!aligned(xq, 16) || !aligned(xs, 4) || !aligned(q, 16) || !aligned(s, 16) || !aligned(y, out) ||
       !aligned(offsets, 4))

@@ -19,6 +19,9 @@
 #include "w4_device.h"
 #include "w4_launch.h"
 #include "w4_rows.h"
+#include "w4_stage.h"
+
+#include <type_traits>
 
 namespace w4 {
 namespace {
@@ -330,88 +333,630 @@ __device__ __forceinline__ void store_value(void* y, int64_t i, float v) {
     static_cast<uint16_t*>(y)[i] = f32_to_bf16_rne(v);
 }
 
-// Streaming form: a block owns R row blocks of 16 outputs and one tile of 16 rows of x;
-// its NW wavefronts divide K.  Lane l of a wavefront holds row l % 16 of x and of the
-// row block, inputs 64 (l / 16) .. + 63 of 256, and D[4 (l / 16) + j][l % 16], j = 0..3,
-// all straight from memory.
-template <int R, int NW, bool kF32>
+// What a block needs to find its operands: buffers of the expert's weights and scales, of
+// the tile's rows of x and their scales, and the sizes they are addressed with.
+struct Operands {
+  __amdgpu_buffer_rsrc_t w, ws, x, xs;
+  int pairs, words, blocks;  // per row: of 256 inputs, of 512, of 32
+};
+
+__device__ __forceinline__ Operands operands_of(const MxArgs& a, const RowTile& rt) {
+  Operands o;
+  o.pairs = (a.K + kPair - 1) / kPair;
+  o.words = (a.K + kWord - 1) / kWord;
+  o.blocks = a.K / kBlock;
+  const uint32_t nb = (uint32_t)(a.N + kTileRows - 1) / kTileRows, rows = (uint32_t)(rt.r1 - rt.r0);
+  const uint32_t codes = nb * (uint32_t)o.pairs * 2048u, scales = nb * (uint32_t)o.words * 256u;
+  o.w = make_rsrc(a.q + (int64_t)rt.expert * codes, codes);
+  o.ws = make_rsrc(a.s + (int64_t)rt.expert * scales, scales);
+  o.x = make_rsrc(a.xq + (int64_t)rt.r0 * (a.K / 2), rows * (uint32_t)(a.K / 2));
+  o.xs = make_rsrc(a.xs + (int64_t)rt.r0 * o.blocks, rows * (uint32_t)o.blocks);
+  return o;
+}
+
+// Streaming form, for few rows: a block owns R row blocks of 16 outputs and one tile of 16
+// rows of x; its NW wavefronts divide K.  Lane l of a wavefront holds row l % 16 of x and of
+// a row block, inputs 64 (l / 16) .. + 63 of 256, and D[4 (l / 16) + j][l % 16], j = 0..3,
+// all straight from memory, D pairs of tiles ahead of the products.
+template <int R, int NW, int kCache, bool kF32>
+__device__ __forceinline__ void stream_row_tile(const MxArgs& a, const RowTile& rt, int rb0, f32x4 (&red)[NW][R][64]) {
+  constexpr int D = 2;
+  const Operands o = operands_of(a, rt);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nl = lane & 15, h = lane >> 4;
+  const int s0 = (int)((int64_t)o.pairs * wave / NW), s1 = (int)((int64_t)o.pairs * (wave + 1) / NW);
+  uint32_t wo[R], wso[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    wo[r] = (uint32_t)(rb0 + r) * (uint32_t)o.pairs * 2048u + 16u * lane;
+    wso[r] = (uint32_t)(rb0 + r) * (uint32_t)o.words * 256u + 4u * lane;
+  }
+  const uint32_t xo = (uint32_t)nl * (uint32_t)(a.K / 2) + 32u * h, xso = (uint32_t)nl * (uint32_t)o.blocks + 2u * h;
+
+  f32x4 acc[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) acc[r] = f32x4{0, 0, 0, 0};
+  // a ring of D pairs' operands; a pair past the wavefront's last, and inputs past K, read zeros
+  // (see kOob), so that every load is unconditional
+  uint4 w[D][R][2], x[D][2];
+  uint32_t sw[D][R], sx[D];
+  auto issue = [&](int c, int s) {
+    const uint32_t ow = s < s1 ? (uint32_t)s * 2048u : kOob, ows = s < s1 ? (uint32_t)(s >> 1) * 256u + 2u * (s & 1) : kOob;
+    const bool there = s < s1 && 8 * s + 2 * h < o.blocks;
+    const uint32_t ox = there ? (uint32_t)s * 128u : kOob, oxs = there ? (uint32_t)s * 8u : kOob;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      w[c][r][0] = bload<kCache>(o.w, wo[r] + ow);
+      w[c][r][1] = bload<kCache>(o.w, wo[r] + ow + 1024u);
+      sw[c][r] = __builtin_amdgcn_raw_buffer_load_b16(o.ws, (int)(wso[r] + ows), 0, 0);
+    }
+    x[c][0] = bload<0>(o.x, xo + ox);
+    x[c][1] = bload<0>(o.x, xo + ox + 16u);
+    sx[c] = __builtin_amdgcn_raw_buffer_load_b16(o.xs, (int)(xso + oxs), 0, 0);
+  };
+#pragma unroll
+  for (int c = 0; c < D; ++c) {
+    issue(c, s0 + c);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  for (int s = s0; s < s1; s += D) {
+#pragma unroll
+    for (int c = 0; c < D; ++c) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        acc[r] = mfma_mx4<0, 0>(x[c][0], w[c][r][0], acc[r], sx[c], sw[c][r]);
+        acc[r] = mfma_mx4<1, 1>(x[c][1], w[c][r][1], acc[r], sx[c], sw[c][r]);
+      }
+      issue(c, s + c + D);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+
+  auto store = [&](int r, const f32x4& v) {
+    const int n = (rb0 + r) * kTileRows + nl;
+    if (n >= a.N) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int m = rt.r0 + 4 * h + j;
+      if (m < rt.r1) store_value<kF32>(a.y, (int64_t)m * a.N + n, v[j]);
+    }
+  };
+  if constexpr (NW == 1) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) store(r, acc[r]);
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r) red[wave][r][lane] = acc[r];
+    __syncthreads();
+    for (int r = wave; r < R; r += NW) {
+      f32x4 v = red[0][r][lane];
+#pragma unroll
+      for (int i = 1; i < NW; ++i) v += red[i][r][lane];
+      store(r, v);
+    }
+  }
+}
+
+// kPast: an expert's weights are read past the caches, unless another row tile of the
+// expert reads them too.
+template <int R, int NW, bool kPast, bool kF32>
 __global__ __launch_bounds__(NW * 64) void mx4_stream_kernel(const MxArgs a) {
   const int nb = (a.N + kTileRows - 1) / kTileRows, panels = (nb + R - 1) / R;
   const int t = blockIdx.x / panels, rb0 = (blockIdx.x - t * panels) * R;
   RowTile rt;
   if (!find_row_tile(a.offsets, a.experts, a.M, 16, t, rt)) return;
   __shared__ f32x4 red[NW][R][64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nl = lane & 15, h = lane >> 4;
-  const int pairs = (a.K + kPair - 1) / kPair, words = (a.K + kWord - 1) / kWord;
-  const int w0 = (int)((int64_t)words * wave / NW), w1 = (int)((int64_t)words * (wave + 1) / NW);
-  const uint32_t codes = (uint32_t)nb * (uint32_t)pairs * 2048u, scales = (uint32_t)nb * (uint32_t)words * 256u;
-  const int rows = rt.r1 - rt.r0;
-  const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.q + (int64_t)rt.expert * codes, codes);
-  const __amdgpu_buffer_rsrc_t rsw = make_rsrc(a.s + (int64_t)rt.expert * scales, scales);
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.xq + (int64_t)rt.r0 * (a.K / 2), (uint32_t)rows * (uint32_t)(a.K / 2));
-  const __amdgpu_buffer_rsrc_t rsx =
-      make_rsrc(a.xs + (int64_t)rt.r0 * (a.K / kBlock), (uint32_t)rows * (uint32_t)(a.K / kBlock));
+  if (kPast && rt.alone) stream_row_tile<R, NW, kNonTemporal, kF32>(a, rt, rb0, red);
+  else stream_row_tile<R, NW, 0, kF32>(a, rt, rb0, red);
+}
 
-  f32x4 acc[R];
+// Sums of TM row tiles of a wavefront, lane l's outputs n0 + 16 (l / 16) .. + 15 of rows
+// m0 + l % 16 + 16 i, stored by way of `stage` (kStageBytes of the wavefront's own).
+template <int TM, bool kF32>
+__device__ __forceinline__ void store_tile(const MxArgs& a, const RowTile& rt, int m0, int n0,
+                                           const f32x4 (&acc)[TM][4], uint8_t* stage) {
+  uint32_t* words = reinterpret_cast<uint32_t*>(stage);
+  const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int r = 0; r < R; ++r) acc[r] = f32x4{0, 0, 0, 0};
-  for (int c = w0; c < w1; ++c) {
-    uint32_t sw[R];
+  for (int i = 0; i < TM; ++i) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      sw[r] = __builtin_amdgcn_raw_buffer_load_b32(rsw, (int)(((uint32_t)(rb0 + r) * words + c) * 256u + 4u * lane), 0, 0);
-    uint4 x[4], w[R][4];
-    uint32_t sx[2];
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int k = c * kWord + p * kPair + 64 * h;  // this lane's first input
-      const bool there = k < a.K;
-      sx[p] = __builtin_amdgcn_raw_buffer_load_b16(
-          rsx, (int)(there ? (uint32_t)(nl * (a.K / kBlock) + k / kBlock) : kOob), 0, 0);
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        x[2 * p + b] = bload<0>(rx, there ? (uint32_t)nl * (uint32_t)(a.K / 2) + (uint32_t)(k / 2 + 16 * b) : kOob);
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-          w[r][2 * p + b] = bload<0>(rw, 2 * c + p < pairs ? (((uint32_t)(rb0 + r) * pairs + 2 * c + p) * 128u + 64u * b + lane) * 16u : kOob);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      acc[r] = mfma_mx4<0, 0>(x[0], w[r][0], acc[r], sx[0], sw[r]);
-      acc[r] = mfma_mx4<1, 1>(x[1], w[r][1], acc[r], sx[0], sw[r]);
-      acc[r] = mfma_mx4<0, 2>(x[2], w[r][2], acc[r], sx[1], sw[r]);
-      acc[r] = mfma_mx4<1, 3>(x[3], w[r][3], acc[r], sx[1], sw[r]);
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < R; ++r) red[wave][r][lane] = acc[r];
-  __syncthreads();
-  for (int r = wave; r < R; r += NW) {
-    const int n = (rb0 + r) * kTileRows + nl;
-    if (n >= a.N) continue;
-    f32x4 v = red[0][r][lane];
-#pragma unroll
-    for (int w_ = 1; w_ < NW; ++w_) v += red[w_][r][lane];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = rt.r0 + 4 * h + j;
-      if (m < rt.r1) store_value<kF32>(a.y, (int64_t)m * a.N + n, v[j]);
-    }
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<f32x4*>(words + (lane & 15) * kStagePitch + 16 * (lane >> 4) + 4 * j) = acc[i][j];
+    store_stage<kF32>(words, a.y, a.N, m0 + 16 * i, rt.r1, n0, [](uint32_t w, int, int) { return __uint_as_float(w); });
   }
 }
 
-struct MxGrid {
+// Tile forms, for more rows: a block of WM x WN wavefronts owns BM = 16 WM TM rows of x and
+// BN = 64 WN outputs; each wavefront holds TM x 4 tiles of 16 x 16 sums in registers.
+// A step is 256 inputs: the block's slices of x and of the weights, and every other step the
+// scales of two, go to LDS straight from memory (no registers in between).
+//
+// x is row-major, 128 bytes of a row per step: eight chunks of 16 bytes, one block each.
+// Block 2 q + t is what lane quarter q multiplies in product t of the step.  It sits at
+// position (q + 4 t) ^ (r % 8) of row r, so that the sixteen rows of an operand are
+// read without bank conflicts.
+//
+// The weights are the first operand, so a lane holds four consecutive rows of it,
+// D[4 (l / 16) + e][l % 16], for one row of x.  Row 4 q + e of tile j of a wavefront's four is
+// output 16 q + 4 j + e: a lane ends with sixteen consecutive outputs of its row.  A row
+// block's 2 KiB of a step are 64 bytes apart from the next one's in LDS, which spreads
+// the four row blocks that one operand touches over the banks.
+//
+// Scales: 16 bytes of a row of x are its blocks' in two steps; the 1 KiB of four row
+// blocks is put in the order in which the operands of tile j read it.  A lane of a row of x
+// takes its bytes from two words of the four; where a pair of steps reaches past K, the
+// bytes of blocks that are not there (the next row's: they could be NaN) become zeros.
+//
+// Rows past the tile's last, row blocks past the matrix's last and inputs past K lie
+// outside their buffers: such loads give zeros (see kOob).  Buffers check each word of a
+// load by itself.
+constexpr int kRowBlockLds = 2 * 1024 + 64;
+
+template <int WM, int WN, int TM>
+struct TileShape {
+  static constexpr int TN = 4, NW = WM * WN, BM = 16 * WM * TM, BN = 16 * WN * TN;
+  static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;    // 1 KiB loads per wavefront and step: x, weights
+  static constexpr int SA = (BM + 63) / 64, SB = BN / 64;      // 1 KiB loads of scales per two steps
+  static constexpr int kSl = (SA + SB + NW - 1) / NW;          // of them per wavefront (some come twice)
+  static constexpr int kX = BM * 128, kBuffer = kX + BN / 16 * kRowBlockLds, kScales = (SA + SB) * 1024;
+  static_assert(LA * NW * 8 == BM && LB * NW * 8 == BN && LB % 2 == 0, "loads shared out evenly");
+};
+
+// Loads and operand reads of a wavefront of a tile (see above).
+template <int WM, int WN, int TM>
+struct TileWave : TileShape<WM, WN, TM> {
+  using S = TileShape<WM, WN, TM>;
+  Operands o;
+  int lane, wave, wm, wn, xblock;
+  uint32_t xo, wo, k_half;              // offsets of the loads
+  uint32_t xa, wa, xsa, wsa;            // and of the reads in LDS
+  uint32_t xsel, xsel_tail;             // bytes of a row's two words that are the lane's scales
+  typedef __attribute__((address_space(3))) void* lds_ptr;
+
+  __device__ __forceinline__ TileWave(const MxArgs& a, const RowTile& rt, int rb0) : o(operands_of(a, rt)) {
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    wm = wave / WN;
+    wn = wave - wm * WN;
+    k_half = (uint32_t)(a.K / 2);
+    rb = rb0;
+    const int nl = lane & 15, kb = lane >> 4, pos = (lane & 7) ^ (lane >> 3);
+    xblock = 2 * (pos & 3) + (pos >> 2);
+    xo = (uint32_t)(8 * wave * S::LA + (lane >> 3)) * k_half + 16u * xblock;
+    wo = (uint32_t)(rb0 + wave * S::LB / 2) * (uint32_t)o.pairs * 2048u + 16u * lane;
+    xa = (uint32_t)(wm * TM * 16 + nl) * 128u + 16u * (kb ^ (nl & 7));
+    wa = (uint32_t)S::kX + (uint32_t)(wn * S::TN + (nl >> 2)) * kRowBlockLds + 256u * kb + 16u * (nl & 3);
+    xsa = (uint32_t)(wm * TM * 16 + nl) * 16u + 4u * (kb >> 1);
+    wsa = (uint32_t)(S::SA + wn) * 1024u + 16u * (4 * (nl >> 2) + kb) + 4u * (nl & 3);
+    const int rest = o.blocks & 15;
+    xsel = kb & 1 ? 0x07060302u : 0x05040100u;
+    xsel_tail = (2 * kb < rest ? xsel & 0xFFFFu : 0x0C0Cu) | (8 + 2 * kb < rest ? xsel & 0xFFFF0000u : 0x0C0C0000u);
+  }
+  // Load i of LA + LB of this wavefront's for step s (zeros past the last step).
+  __device__ __forceinline__ void load(int i, int s, uint8_t* to) const {
+    if (i < S::LA) {
+      const uint32_t k = 8 * s + xblock < o.blocks ? (uint32_t)s * 128u : kOob;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(o.x, (lds_ptr)(to + (wave * S::LA + i) * 1024), 16,
+                                               (int)(xo + (uint32_t)(8 * i) * k_half + k), 0, 0, 0);
+    } else {
+      const uint32_t k = s < o.pairs ? (uint32_t)s * 2048u : kOob;
+      const int r = (i - S::LA) >> 1, t = (i - S::LA) & 1;  // row block, tile
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          o.w, (lds_ptr)(to + S::kX + (wave * S::LB / 2 + r) * kRowBlockLds + t * 1024), 16,
+          (int)(wo + (uint32_t)(r * o.pairs) * 2048u + 1024u * t + k), 0, 0, 0);
+    }
+  }
+  // The scales of steps s and s + 1 (s even).
+  __device__ __forceinline__ void load_scales(int s, uint8_t* to) const {
+#pragma unroll
+    for (int i = 0; i < S::kSl; ++i) {
+      const int u = (wave * S::kSl + i) % (S::SA + S::SB);
+      const bool of_x = u < S::SA;
+      const __amdgpu_buffer_rsrc_t rs = of_x ? o.xs : o.ws;
+      const uint32_t so = of_x ? (uint32_t)(64 * u + lane) * (uint32_t)o.blocks
+                               : (uint32_t)(rb + 4 * (u - S::SA) + ((lane >> 2) & 3)) * (uint32_t)o.words * 256u +
+                                     16u * (4 * (lane & 3) + (lane >> 4));
+      const uint32_t k = s < o.pairs ? (uint32_t)s << (of_x ? 3 : 7) : kOob;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(to + u * 1024), 16, (int)(so + k), 0, 0, 0);
+    }
+  }
+  __device__ __forceinline__ uint4 read_w(int t, int j, const uint8_t* from) const {
+    return *reinterpret_cast<const uint4*>(from + wa + j * 64 + t * 1024);
+  }
+  __device__ __forceinline__ uint4 read_x(int t, int i, const uint8_t* from) const {
+    return *reinterpret_cast<const uint4*>(from + (xa ^ (64u * t)) + i * 2048);
+  }
+  __device__ __forceinline__ uint32_t read_ws(int j, const uint8_t* from) const {
+    return *reinterpret_cast<const uint32_t*>(from + wsa + j * 256);
+  }
+  __device__ __forceinline__ void read_xs(int i, const uint8_t* from, uint32_t (&to)[2]) const {
+    const uint32_t* at = reinterpret_cast<const uint32_t*>(from + xsa + i * 256);
+    to[0] = at[0];
+    to[1] = at[2];
+  }
+  // The lane's four scales of a row of x for steps s and s + 1, of what read_xs read.
+  __device__ __forceinline__ uint32_t take_xs(int s, const uint32_t (&v)[2]) const {
+    return __builtin_amdgcn_perm(v[1], v[0], 8 * s + 16 > o.blocks ? xsel_tail : xsel);
+  }
+  int rb;
+};
+
+typedef std::integral_constant<int, 0> Zero;
+typedef std::integral_constant<int, 1> One;
+
+__device__ __forceinline__ void operands_ready() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Every read of LDS that this wavefront has issued is done, and so are its loads into LDS but
+// for the last `left`; and so are the other wavefronts'.
+template <int kLeft>
+__device__ __forceinline__ void all_done() {
+  static_assert(kLeft < 64, "vmcnt");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (kLeft & 15) | (kLeft >> 4) << 14);  // vmcnt(kLeft) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Many rows: two buffers, loads one step ahead.  The products of a step run in four parts
+// (half of the rows times one of the two products).  Operands are read from LDS one
+// part ahead, beside the products of the part before; the next step's loads are issued
+// beside the first two parts, as one load holds up the wavefront while the address unit of
+// the CU takes it.  kAhead: a share of the lines that the step after next needs is touched
+// early, so that its loads find them in the L2 of the XCD: share `share_x` of eight of
+// the rows and `share_w` of four of the row blocks, as the blocks that run at one time on an XCD
+// hold four row tiles times eight panels (tile_of_block).
+template <int WM, int WN, int TM, bool kAhead, bool kF32, int L0, int L1, int LS>
+__device__ __forceinline__ void run_tile(const MxArgs& a, const RowTile& rt, int rb0, int share_x, int share_w,
+                                         uint8_t (&lds0)[L0], uint8_t (&lds1)[L1], uint8_t (&scales)[LS],
+                                         uint8_t* touched) {
+  using S = TileShape<WM, WN, TM>;
+  constexpr int TN = S::TN, TH = TM / 2, NW = S::NW;
+  static_assert(TH * 2 == TM && (S::LA + S::LB) % 2 == 0 && S::kSl == 1, "parts");
+  static_assert(S::kBuffer <= L0 && S::kBuffer <= L1 && S::kScales <= LS, "buffers");
+  const TileWave<WM, WN, TM> tw(a, rt, rb0);
+  const int steps = tw.o.pairs;
+  const bool touch_x = tw.wave < NW / 2;
+  const __amdgpu_buffer_rsrc_t touch_rs = touch_x ? tw.o.x : tw.o.w;
+  const uint32_t touch_at =
+      touch_x ? (tw.lane < S::BM / 4 / NW ? (uint32_t)(S::BM / 8 * share_x + S::BM / 4 / NW * tw.wave + tw.lane) * tw.k_half : kOob)
+              : (tw.lane < 16 ? (uint32_t)(rb0 + S::BN / 64 * share_w + tw.wave - NW / 2) * (uint32_t)steps * 2048u + 128u * tw.lane
+                              : kOob);
+  auto touch = [&](int s) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(touch_rs, (typename TileWave<WM, WN, TM>::lds_ptr)(touched + tw.wave * 256), 4,
+                                             (int)(touch_at + ((uint32_t)min(s, steps - 1) << (touch_x ? 7 : 11))), 0, 0, 0);
+  };
+
+  f32x4 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  uint4 x[2][TH], w[2][TN];  // x by row half, w by product
+  uint32_t sx[2][TH], sx_read[TH][2], sw[TN], sw_read[TN];
+  // the products t of row half c of a step of parity P; beside(i) comes before row tile i's
+  auto multiply = [&](auto parity, auto product, int c, auto beside) {
+    constexpr int t = decltype(product)::value, kByte = 2 * decltype(parity)::value + t;
+#pragma unroll
+    for (int i = 0; i < TH; ++i) {
+      beside(i);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        acc[c * TH + i][j] = mfma_mx4<kByte, kByte>(w[t][j], x[c][i], acc[c * TH + i][j], sw[j], sx[c][i]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // A step of parity P whose slices are in `cur`, with the last part of the step before; its
+  // own last part is left to the next.
+  auto step = [&](auto parity, auto other, int s, uint8_t* cur, uint8_t* nxt) {
+    constexpr bool even = decltype(parity)::value == 0;
+    constexpr int kReads = TN + TH, kHalf = (S::LA + S::LB) / 2;
+    auto read = [&](int t, int i) {  // share i of TH of product t's operands
+#pragma unroll
+      for (int r = (i * kReads + TH - 1) / TH; r < ((i + 1) * kReads + TH - 1) / TH; ++r) {
+        if (r < TN) w[t][r] = tw.read_w(t, r, cur);
+        else x[0][r - TN] = tw.read_x(t, r - TN, cur);
+      }
+    };
+    auto load = [&](int half, int i) {
+#pragma unroll
+      for (int l = half * kHalf + i * kHalf / TH; l < half * kHalf + (i + 1) * kHalf / TH; ++l) tw.load(l, s + 1, nxt);
+    };
+    all_done<kAhead ? 1 : 0>();  // `cur` is filled, and nothing reads `nxt` any more
+    multiply(other, One(), 1, [&](int i) {
+      load(0, i);
+      if (!even && i == 0) tw.load_scales(s + 1, scales);
+      read(0, i);
+      if constexpr (even) {
+        tw.read_xs(i, scales, sx_read[i]);
+#pragma unroll
+        for (int j = i * TN / TH; j < (i + 1) * TN / TH; ++j) sw_read[j] = tw.read_ws(j, scales);
+      }
+    });
+    operands_ready();
+    if constexpr (even) {
+#pragma unroll
+      for (int i = 0; i < TH; ++i) sx[0][i] = tw.take_xs(s, sx_read[i]);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) sw[j] = sw_read[j];
+    }
+    multiply(parity, Zero(), 0, [&](int i) {
+      load(1, i);
+      x[1][i] = tw.read_x(0, TH + i, cur);
+      if constexpr (even) tw.read_xs(TH + i, scales, sx_read[i]);
+    });
+    operands_ready();
+    if constexpr (even) {
+#pragma unroll
+      for (int i = 0; i < TH; ++i) sx[1][i] = tw.take_xs(s, sx_read[i]);
+    }
+    multiply(parity, Zero(), 1, [&](int i) {
+      if (kAhead && i == 0) touch(s + 2);  // the last of the step: what all_done leaves in flight
+      read(1, i);
+    });
+    operands_ready();
+    multiply(parity, One(), 0, [&](int i) { x[1][i] = tw.read_x(1, TH + i, cur); });
+  };
+
+#pragma unroll
+  for (int i = 0; i < S::LA + S::LB; ++i) tw.load(i, 0, lds0);
+  tw.load_scales(0, scales);
+  if constexpr (kAhead) touch(1);
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {  // no step before the first
+    w[1][j] = make_uint4(0, 0, 0, 0);
+    sw[j] = 0;
+  }
+#pragma unroll
+  for (int i = 0; i < TH; ++i) {
+    x[1][i] = make_uint4(0, 0, 0, 0);
+    sx[1][i] = 0;
+  }
+  for (int s = 0; s < steps; s += 2) {  // an odd last step is followed by one of zeros
+    step(Zero(), One(), s, lds0, lds1);
+    step(One(), Zero(), s + 1, lds1, lds0);
+  }
+  multiply(One(), One(), 1, [](int) {});
+  all_done<0>();  // no load into LDS is left, and nothing reads what the stages overwrite
+  static_assert(NW * kStageBytes <= L0, "stages fit a buffer");
+  store_tile<TM, kF32>(a, rt, rt.r0 + 16 * tw.wm * TM, 16 * rb0 + 64 * tw.wn, acc, lds0 + tw.wave * kStageBytes);
+}
+
+// 256 x 256 per block of eight wavefronts, one block per CU.  What is left of the tiles
+// after whole rounds of kCus, if at most a quarter of a round, is cut into four tiles of 128 x
+// 128 each, which fill another round in less than half the time of whole tiles; a tile
+// of at most 128 rows (an expert's last) is half as high.
+constexpr int kCus = 256, kMostCut = kCus / 4;
+
+template <bool kF32>
+__global__ __launch_bounds__(512, 1) void mx4_tile_kernel(const MxArgs a, int panels) {
+  using Whole = TileShape<2, 4, 8>;
+  // variables of their own, each named outright where it is used: the compiler then knows
+  // that loads into one are no reason to wait before reading another
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[Whole::kBuffer], lds1[Whole::kBuffer], scales[Whole::kScales];
+  __shared__ uint8_t touched[Whole::NW * 256];
+  const int tiles = count_row_tiles(a.offsets, a.experts, a.M, 256);
+  // (offsets whose ranges overlap could make more tiles than the launch covers)
+  const int total = min(tiles, ((int)gridDim.x - 3 * kMostCut) / panels) * panels;
+  const int cut = total % kCus <= kMostCut ? total % kCus : 0;
+  int b = blockIdx.x, quarter = -1;
+  if (b >= total - cut) {
+    const int i = b - (total - cut);
+    quarter = i & 3;
+    b = total - cut + (i >> 2);
+    if (b >= total) return;
+  }
+  int t, p;
+  tile_of_block(b, total / panels, panels, t, p);
+  RowTile rt;
+  if (!find_row_tile(a.offsets, a.experts, a.M, 256, t, rt)) return;
+  if (quarter >= 0) {
+    const int rb0 = 16 * p + 8 * (quarter & 1);
+    rt.r0 += 128 * (quarter >> 1);
+    rt.r1 = min(rt.r1, rt.r0 + 128);
+    if (rt.r0 < rt.r1 && rb0 * kTileRows < a.N) run_tile<4, 2, 2, false, kF32>(a, rt, rb0, 0, 0, lds0, lds1, scales, touched);
+  } else if (rt.r1 - rt.r0 <= 128) {
+    run_tile<2, 4, 4, true, kF32>(a, rt, 16 * p, p & 7, t & 3, lds0, lds1, scales, touched);
+  } else {
+    run_tile<2, 4, 8, true, kF32>(a, rt, 16 * p, p & 7, t & 3, lds0, lds1, scales, touched);
+  }
+}
+
+// Fewer rows, where each block's time is the latency of its loads: smaller tiles, four
+// buffers, loads three steps ahead, two parts (one product each) per step.
+template <int WM, int WN, int TM, bool kF32>
+__global__ __launch_bounds__(WM* WN * 64) void mx4_deep_kernel(const MxArgs a, int panels) {
+  using S = TileShape<WM, WN, TM>;
+  constexpr int TN = S::TN;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[S::kBuffer], lds1[S::kBuffer], lds2[S::kBuffer], lds3[S::kBuffer],
+      scales0[S::kScales], scales2[S::kScales];
+  // (offsets whose ranges overlap could make more tiles than the launch covers)
+  const int tiles = min(count_row_tiles(a.offsets, a.experts, a.M, S::BM), (int)gridDim.x / panels);
+  if ((int)blockIdx.x >= tiles * panels) return;
+  int t, p;
+  tile_of_block(blockIdx.x, tiles, panels, t, p);
+  RowTile rt;
+  if (!find_row_tile(a.offsets, a.experts, a.M, S::BM, t, rt)) return;
+  const int rb0 = p * (S::BN / 16);
+  const TileWave<WM, WN, TM> tw(a, rt, rb0);
+  const int steps = tw.o.pairs;
+
+  f32x4 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  uint4 x[2][TM], w[2][TN];  // by product
+  uint32_t sx[TM], sx_read[TM][2], sw[TN], sw_read[TN];
+  auto multiply = [&](auto parity, auto product, auto beside) {
+    constexpr int q = decltype(product)::value, kByte = 2 * decltype(parity)::value + q;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      beside(i);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = mfma_mx4<kByte, kByte>(w[q][j], x[q][i], acc[i][j], sw[j], sx[i]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // A step of parity P: `far` is loaded for step s + 3 (with scales, where that is even).
+  auto step = [&](auto parity, auto other, int s, uint8_t* cur, uint8_t* far, uint8_t* cur_scales, uint8_t* far_scales) {
+    constexpr bool even = decltype(parity)::value == 0;
+    constexpr int kLoads = S::LA + S::LB, kReads = TN + TM;
+    auto read = [&](int q, int i) {  // share i of TM of product q's operands
+#pragma unroll
+      for (int r = (i * kReads + TM - 1) / TM; r < ((i + 1) * kReads + TM - 1) / TM; ++r) {
+        if (r < TN) w[q][r] = tw.read_w(q, r, cur);
+        else x[q][r - TN] = tw.read_x(q, r - TN, cur);
+      }
+    };
+    all_done<2 * kLoads + S::kSl>();  // all but the loads of the next two steps
+    multiply(other, One(), [&](int i) {
+#pragma unroll
+      for (int l = i * kLoads / TM; l < (i + 1) * kLoads / TM; ++l) tw.load(l, s + 3, far);
+      if (!even && i == TM - 1) tw.load_scales(s + 3, far_scales);
+      read(0, i);
+      if constexpr (even) {
+        tw.read_xs(i, cur_scales, sx_read[i]);
+#pragma unroll
+        for (int j = i * TN / TM; j < (i + 1) * TN / TM; ++j) sw_read[j] = tw.read_ws(j, cur_scales);
+      }
+    });
+    operands_ready();
+    if constexpr (even) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i) sx[i] = tw.take_xs(s, sx_read[i]);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) sw[j] = sw_read[j];
+    }
+    multiply(parity, Zero(), [&](int i) { read(1, i); });
+  };
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {  // no step before the first
+    w[1][j] = make_uint4(0, 0, 0, 0);
+    sw[j] = 0;
+  }
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    x[1][i] = make_uint4(0, 0, 0, 0);
+    sx[i] = 0;
+  }
+  auto load_step = [&](int s, uint8_t* to) {
+#pragma unroll
+    for (int i = 0; i < S::LA + S::LB; ++i) tw.load(i, s, to);
+  };
+  load_step(0, lds0);
+  tw.load_scales(0, scales0);
+  load_step(1, lds1);
+  load_step(2, lds2);
+  tw.load_scales(2, scales2);
+  for (int s = 0; s < steps; s += 4) {  // steps past the last are of zeros
+    step(Zero(), One(), s, lds0, lds3, scales0, nullptr);
+    step(One(), Zero(), s + 1, lds1, lds0, nullptr, scales0);
+    step(Zero(), One(), s + 2, lds2, lds1, scales2, nullptr);
+    step(One(), Zero(), s + 3, lds3, lds2, nullptr, scales2);
+  }
+  operands_ready();
+  multiply(One(), One(), [](int) {});
+  all_done<0>();  // no load into LDS is left, and nothing reads what the stages overwrite
+  static_assert((S::NW + 1) / 2 * kStageBytes <= S::kBuffer, "stages fit two buffers");
+  store_tile<TM, kF32>(a, rt, rt.r0 + 16 * tw.wm * TM, 16 * rb0 + 64 * tw.wn, acc,
+                       (tw.wave & 1 ? lds1 : lds0) + (tw.wave >> 1) * kStageBytes);
+}
+
+// ---------------------------------------------------------------------------
+// launch configuration
+// ---------------------------------------------------------------------------
+enum class Mx4 { kTile256, kDeep128, kDeep64x128, kDeep64, kDeep32x64, kStream1x4, kStream2x4, kStream2x2, kStream2x1 };
+
+struct Mx4Shape {
+  Mx4 kind;
   int BM, BN, threads;
+  // the estimate of a call's time, us: start + (steps of 256 inputs) * max(one, all * blocks / slots)
+  int slots;
+  double start, one, all;
+};
+// Fitted to the times of 2560 x 9216, 9216 x 2560, 5120 x 5120, 17408 x 5120, 28672 x 8192, 1024 x 2048
+// and 2048 x 1408 at 17 to 4096 rows (other weights than the last call's; within 7 to 17%).
+constexpr Mx4Shape kMx4Shapes[] = {
+    {Mx4::kTile256, 256, 256, 512, 256, 2.1, 0.15, 1.87},   {Mx4::kDeep128, 128, 128, 256, 256, 5.3, 0.34, 0.80},
+    {Mx4::kDeep64x128, 64, 128, 256, 256, 4.3, 0.23, 0.54}, {Mx4::kDeep64, 64, 64, 256, 512, 3.8, 0.16, 0.60},
+    {Mx4::kDeep32x64, 32, 64, 128, 512, 3.5, 0.13, 0.43},   {Mx4::kStream2x4, 16, 32, 256, 1024, 2.3, 0.14, 0.75},
+    {Mx4::kStream2x2, 16, 32, 128, 2048, 2.2, 0.13, 1.36},  {Mx4::kStream2x1, 16, 32, 64, 4096, 1.6, 0.25, 2.58},
+    {Mx4::kStream1x4, 16, 16, 256, 0, 0, 0, 0},
+};
+
+// The kernel for M rows shared out over `experts` matrices of N x K (their true sizes are on
+// the GPU: all are taken to be as busy as the average one).  Up to 16 rows each the
+// streaming form with as many wavefronts as there are few outputs (us, one row: 2560 x 9216 as
+// one row block and four wavefronts 4.6, as two and four 5.1, two and two 6.1, two and
+// one 13; 5120 x 5120 5.5, 4.8, 4.7, 8.3; 9216 x 2560 5.3, 5.5, 4.8, 5.5; 13 rows of 28672 x 8192
+// 32.4, 29.0, 26.8, 23.1).  Beyond that the smallest estimate.  512 rows: 2560 x 9216 take 14.6 us as
+// 64 x 128 (160 blocks), 18.5 as 64 x 64, 19.2 as 128 x 128 and 33 as 256 x 256 (20 blocks);
+// 17408 x 5120 60, 58, 52 and 41 us.
+Mx4 choose_mx4(int64_t M, int64_t N, int64_t K, int64_t experts) {
+  const int64_t busy = experts < M ? experts : M, rows = (M + busy - 1) / busy;
+  const int64_t nb = (N + kTileRows - 1) / kTileRows * busy, steps = (K + kPair - 1) / kPair;
+  if (rows <= 16) return nb < 256 ? Mx4::kStream1x4 : nb < 384 ? Mx4::kStream2x4 : nb < 1024 ? Mx4::kStream2x2 : Mx4::kStream2x1;
+  Mx4 best = Mx4::kTile256;
+  double least = 0;
+  for (const Mx4Shape& s : kMx4Shapes) {
+    if (s.slots == 0) continue;
+    const int64_t blocks = busy * ((rows + s.BM - 1) / s.BM) * ((N + s.BN - 1) / s.BN);
+    double load = (double)blocks / s.slots;
+    if (s.kind == Mx4::kTile256) {  // whole rounds, the last one cut
+      const int64_t left = blocks % kCus;
+      load = (double)(blocks / kCus) + (left == 0 ? 0 : left <= kMostCut ? 0.45 : 1);
+    }
+    const double cost = s.start + (double)steps * (load * s.all > s.one ? load * s.all : s.one);
+    if (least == 0 || cost < least) {
+      least = cost;
+      best = s.kind;
+    }
+  }
+  return best;
+}
+
+// The kernel of a call, and its grid.
+struct MxGrid {
+  Mx4 kind;
+  int threads;
   int64_t panels, blocks;
 };
 
-MxGrid mx4_grid(int64_t M, int64_t N, int64_t experts, bool grouped) {
-  MxGrid g{16, 32, 128, 0, 0};
-  g.panels = (N + g.BN - 1) / g.BN;
-  g.blocks = max_row_tiles(M, experts, grouped, g.BM) * g.panels;
+MxGrid mx4_grid(int64_t M, int64_t N, int64_t K, int64_t experts, bool grouped) {
+  const Mx4 kind = choose_mx4(M, N, K, experts);
+  MxGrid g{kind, 0, 0, 0};
+  for (const Mx4Shape& s : kMx4Shapes)
+    if (s.kind == kind) {
+      g.threads = s.threads;
+      g.panels = (N + s.BN - 1) / s.BN;
+      g.blocks = max_row_tiles(M, experts, grouped, s.BM) * g.panels + (kind == Mx4::kTile256 ? 3 * kMostCut : 0);
+    }
   return g;
+}
+
+template <bool kF32>
+hipError_t launch_product(const MxArgs& a, hipStream_t st) {
+  const MxGrid g = mx4_grid(a.M, a.N, a.K, a.experts, a.offsets != nullptr);
+  const unsigned blocks = (unsigned)g.blocks;
+  const int panels = (int)g.panels;
+  switch (g.kind) {
+    case Mx4::kTile256: mx4_tile_kernel<kF32><<<blocks, 512, 0, st>>>(a, panels); break;
+    case Mx4::kDeep128: mx4_deep_kernel<2, 2, 4, kF32><<<blocks, 256, 0, st>>>(a, panels); break;
+    case Mx4::kDeep64x128: mx4_deep_kernel<2, 2, 2, kF32><<<blocks, 256, 0, st>>>(a, panels); break;
+    case Mx4::kDeep64: mx4_deep_kernel<4, 1, 1, kF32><<<blocks, 256, 0, st>>>(a, panels); break;
+    case Mx4::kDeep32x64: mx4_deep_kernel<2, 1, 1, kF32><<<blocks, 128, 0, st>>>(a, panels); break;
+    case Mx4::kStream1x4: mx4_stream_kernel<1, 4, false, kF32><<<blocks, 256, 0, st>>>(a); break;
+    case Mx4::kStream2x4: mx4_stream_kernel<2, 4, false, kF32><<<blocks, 256, 0, st>>>(a); break;
+    case Mx4::kStream2x2: mx4_stream_kernel<2, 2, false, kF32><<<blocks, 128, 0, st>>>(a); break;
+    case Mx4::kStream2x1: mx4_stream_kernel<2, 1, true, kF32><<<blocks, 64, 0, st>>>(a); break;
+  }
+  return hipGetLastError();
 }
 
 // Wavefronts of one launch of the kernels that give each a piece of work: less than 2^31
@@ -492,8 +1037,8 @@ hipError_t launch_dequantize_tokens_mx4(const uint8_t* xq, const uint8_t* xs, in
   });
 }
 
-bool fits_linear_mx4(int64_t M, int64_t N, int64_t experts, bool grouped) {
-  const MxGrid g = mx4_grid(M, N, experts, grouped);
+bool fits_linear_mx4(int64_t M, int64_t N, int64_t K, int64_t experts, bool grouped) {
+  const MxGrid g = mx4_grid(M, N, K, experts, grouped);
   return g.blocks * g.threads < kMaxThreads;
 }
 
@@ -501,11 +1046,7 @@ hipError_t launch_linear_mx4(const uint8_t* xq, const uint8_t* xs, int64_t M, in
                              int64_t experts, const uint8_t* q, const uint8_t* s, int64_t N, void* y, bool f32,
                              hipStream_t st) {
   const MxArgs a{xq, xs, offsets, q, s, y, (int)M, (int)K, (int)N, (int)experts};
-  const MxGrid g = mx4_grid(M, N, experts, offsets != nullptr);
-  const unsigned blocks = (unsigned)g.blocks;
-  if (f32) mx4_stream_kernel<2, 2, true><<<blocks, 128, 0, st>>>(a);
-  else mx4_stream_kernel<2, 2, false><<<blocks, 128, 0, st>>>(a);
-  return hipGetLastError();
+  return f32 ? launch_product<true>(a, st) : launch_product<false>(a, st);
 }
 
 }  // namespace w4

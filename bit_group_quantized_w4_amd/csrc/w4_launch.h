@@ -192,7 +192,7 @@ hipError_t launch_quantize_tokens_mx4(const void* x, bool f32, int64_t M, int64_
 hipError_t launch_dequantize_tokens_mx4(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, void* x, bool f32,
                                         hipStream_t stream);
 // y = x^ w^T; offsets as for launch_linear_w8a8.
-bool fits_linear_mx4(int64_t M, int64_t N, int64_t experts, bool grouped);  // the tiles fit a launch
+bool fits_linear_mx4(int64_t M, int64_t N, int64_t K, int64_t experts, bool grouped);  // the tiles fit a launch
 hipError_t launch_linear_mx4(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, const int32_t* offsets,
                              int64_t experts, const uint8_t* q, const uint8_t* s, int64_t N, void* y, bool f32,
                              hipStream_t stream);
