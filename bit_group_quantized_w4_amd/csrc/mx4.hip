@@ -880,18 +880,19 @@ struct Mx4Shape {
   int slots;
   double start, one, all;
 };
-// Fitted to the times of 2560 x 9216, 9216 x 2560, 5120 x 5120, 17408 x 5120, 28672 x 8192, 1024 x 2048
-// and 2048 x 1408 at 17 to 4096 rows (other weights than the last call's; within 7 to 17%).
+// Constants that lose least by the choice over the times of all these kernels on 14 matrices (N from
+// 300 to 28672, K from 128 to 9216) at 17 to 4096 rows, other weights than the last call's: 1.5% on
+// average against the best of them each time, 26% at most.
 constexpr Mx4Shape kMx4Shapes[] = {
-    {Mx4::kTile256, 256, 256, 512, 256, 2.1, 0.15, 1.87},   {Mx4::kDeep128, 128, 128, 256, 256, 5.3, 0.34, 0.80},
-    {Mx4::kDeep64x128, 64, 128, 256, 256, 4.3, 0.23, 0.54}, {Mx4::kDeep64, 64, 64, 256, 512, 3.8, 0.16, 0.60},
-    {Mx4::kDeep32x64, 32, 64, 128, 512, 3.5, 0.13, 0.43},   {Mx4::kStream2x4, 16, 32, 256, 1024, 2.3, 0.14, 0.75},
-    {Mx4::kStream2x2, 16, 32, 128, 2048, 2.2, 0.13, 1.36},  {Mx4::kStream2x1, 16, 32, 64, 4096, 1.6, 0.25, 2.58},
+    {Mx4::kTile256, 256, 256, 512, 256, 3.4, 0, 1.77},      {Mx4::kDeep128, 128, 128, 256, 256, 6.3, 0.48, 0.66},
+    {Mx4::kDeep64x128, 64, 128, 256, 256, 8.9, 0, 0.363},   {Mx4::kDeep64, 64, 64, 256, 512, 3.7, 0.196, 0.666},
+    {Mx4::kDeep32x64, 32, 64, 128, 512, 3.7, 0.173, 0.393}, {Mx4::kStream2x2, 16, 32, 128, 2048, 2.5, 0, 1.76},
+    {Mx4::kStream2x1, 16, 32, 64, 4096, 2.5, 0.234, 2.87},  {Mx4::kStream2x4, 16, 32, 256, 0, 0, 0, 0},
     {Mx4::kStream1x4, 16, 16, 256, 0, 0, 0, 0},
 };
 
 // The kernel for M rows shared out over `experts` matrices of N x K (their true sizes are on
-// the GPU: all are taken to be as busy as the average one).  Up to 16 rows each the
+// the GPU).  Up to 16 rows each the
 // streaming form with as many wavefronts as there are few outputs (us, one row: 2560 x 9216 as
 // one row block and four wavefronts 4.6, as two and four 5.1, two and two 6.1, two and
 // one 13; 5120 x 5120 5.5, 4.8, 4.7, 8.3; 9216 x 2560 5.3, 5.5, 4.8, 5.5; 13 rows of 28672 x 8192
@@ -906,7 +907,10 @@ Mx4 choose_mx4(int64_t M, int64_t N, int64_t K, int64_t experts) {
   double least = 0;
   for (const Mx4Shape& s : kMx4Shapes) {
     if (s.slots == 0) continue;
-    const int64_t blocks = busy * ((rows + s.BM - 1) / s.BM) * ((N + s.BN - 1) / s.BN);
+    // experts are not evenly busy: half a row tile more for each
+    const int64_t spread = M / s.BM + busy / 2;
+    const int64_t tiles = busy == 1 ? (M + s.BM - 1) / s.BM : spread > busy ? spread : busy;
+    const int64_t blocks = tiles * ((N + s.BN - 1) / s.BN);
     double load = (double)blocks / s.slots;
     if (s.kind == Mx4::kTile256) {  // whole rounds, the last one cut
       const int64_t left = blocks % kCus;
