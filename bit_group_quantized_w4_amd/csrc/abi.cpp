@@ -1209,15 +1209,15 @@ w4_status w4_linear_grouped_mx4_f32(const uint8_t* xq, const uint8_t* xs, int64_
 // ---------------------------------------------------------------------------
 size_t w4_expert_sort_workspace_bytes(int64_t tokens, int64_t top, int64_t experts) {
   if (!slots_ok(tokens, top) || !experts_ok(experts)) return 0;
-  return w4::expert_sort_workspace(tokens * top, experts);
+  return w4::expert_sort_workspace(tokens, top, experts);
 }
 
 w4_status w4_expert_sort(const void* ids, int id_bytes, int64_t tokens, int64_t top, int64_t experts, int32_t* offsets,
                          int32_t* place, int32_t* order, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   if (w4_status e = check_sort(ids, id_bytes, tokens, top, experts, offsets, place, order, workspace, workspace_bytes))
     return e;
-  return hip_status(w4::launch_expert_sort(ids, id_bytes == 8, tokens * top, experts, offsets, place, order, workspace,
-                                           stream));
+  return hip_status(w4::launch_expert_dispatch(nullptr, 0, ids, id_bytes == 8, tokens, top, experts, offsets, place, order,
+                                               nullptr, workspace, stream));
 }
 
 w4_status w4_expert_take(const void* x, int64_t tokens, int64_t row_bytes, int64_t top, const int32_t* offsets,
@@ -1247,11 +1247,8 @@ w4_status w4_expert_dispatch(const void* x, int64_t row_bytes, const void* ids, 
     const Span in[] = {{x, (size_t)tokens * row_bytes}, {ids, (size_t)id_bytes * slots}};
     if (any_overlap(out, 5, in, 2)) return W4_ERR_ARG;
   }
-  if (w4_status e = hip_status(w4::launch_expert_sort(ids, id_bytes == 8, tokens * top, experts, offsets, place, order,
-                                                      workspace, stream)))
-    return e;
-  if (tokens == 0 || row_bytes == 0) return W4_OK;
-  return hip_status(w4::launch_expert_take(x, tokens, row_bytes, top, offsets, experts, place, xs, stream));
+  return hip_status(w4::launch_expert_dispatch(x, tokens ? row_bytes : 0, ids, id_bytes == 8, tokens, top, experts, offsets,
+                                               place, order, xs, workspace, stream));
 }
 
 w4_status w4_expert_combine(const void* y, int y_type, const void* weights, int weights_type, int64_t tokens, int64_t top,

@@ -198,10 +198,11 @@ hipError_t launch_linear_mx4(const uint8_t* xq, const uint8_t* xs, int64_t M, in
                              hipStream_t stream);
 
 // Rows to the experts and back (experts.hip).  slots = tokens * top.
-size_t expert_sort_workspace(int64_t slots, int64_t experts);
-// ids int64 (wide) or int32 [slots].
-hipError_t launch_expert_sort(const void* ids, bool wide, int64_t slots, int64_t experts, int32_t* offsets, int32_t* place,
-                              int32_t* order, void* workspace, hipStream_t stream);
+size_t expert_sort_workspace(int64_t tokens, int64_t top, int64_t experts);
+// ids int64 (wide) or int32 [tokens][top]; then the rows (bytes 0: none) as launch_expert_take.
+hipError_t launch_expert_dispatch(const void* x, int64_t bytes, const void* ids, bool wide, int64_t tokens, int64_t top,
+                                  int64_t experts, int32_t* offsets, int32_t* place, int32_t* order, void* xs,
+                                  void* workspace, hipStream_t stream);
 // Rows of `bytes` bytes: xs[place[t][j]] = x[t], zeros from row offsets[experts] on.
 hipError_t launch_expert_take(const void* x, int64_t tokens, int64_t bytes, int64_t top, const int32_t* offsets,
                               int64_t experts, const int32_t* place, void* xs, hipStream_t stream);

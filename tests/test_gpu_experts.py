@@ -93,7 +93,7 @@ DTYPES = {"bf16": BF16, "f32": F32, "u8": torch.uint8, "i8": torch.int8}
 
 @pytest.mark.parametrize("dtype", sorted(DTYPES))
 @pytest.mark.parametrize("T,top,E,K", [(1, 1, 1, 1), (8, 2, 64, 2560), (9, 3, 5, 77), (40, 4, 16, 7), (33, 8, 64, 1409),
-                                       (200, 2, 9, 130), (2000, 3, 40, 16), (1500, 8, 128, 33), (3, 2, 4, 20000)])
+                                       (200, 2, 9, 130), (1200, 3, 16, 640), (2000, 3, 40, 16), (1500, 8, 128, 33), (3, 2, 4, 20000)])
 def test_dispatch_and_take(w4, gpu, T, top, E, K, dtype):
     rng = np.random.default_rng(T + K)
     for kind in ("random", "dropped", "none"):
@@ -126,7 +126,7 @@ def test_take_of_scales(w4, gpu):
     assert np.array_equal(got.cpu().numpy(), oracle.expert_take_ref(sx, rows.place.cpu().numpy()))
 
 
-COMBINES = [(1, 1, 1, 1), (8, 2, 64, 2560), (9, 3, 5, 77), (40, 4, 16, 7), (33, 8, 64, 1409), (200, 2, 9, 130), (70, 10, 20, 264),
+COMBINES = [(1, 1, 1, 1), (1200, 3, 16, 640), (1100, 2, 16, 1027), (8, 2, 64, 2560), (9, 3, 5, 77), (40, 4, 16, 7), (33, 8, 64, 1409), (200, 2, 9, 130), (70, 10, 20, 264),
             (1500, 8, 128, 33), (3, 2, 4, 20000), (500, 1, 8, 512), (2, 70, 100, 100)]
 
 
