@@ -9,6 +9,7 @@ been built (build it with ``python -m bit_group_quantized_w4_amd._build``).
 """
 
 import ctypes
+import functools
 import os
 import typing
 
@@ -990,14 +991,16 @@ def _ids(experts, E):
     return dev, T, top, experts.element_size()
 
 
+@functools.lru_cache(maxsize=256)
+def _sort_bytes(T, top, E):
+    return int(_lib.w4_expert_sort_workspace_bytes(T, top, E))
+
+
 def _empty_rows(T, top, E, device):
     """(ExpertRows to be filled, workspace, its bytes)."""
-    nb = _lib.w4_expert_sort_workspace_bytes(T, top, E)
-    # one allocation: offsets, place, order, and the workspace behind them
-    slots = T * top
-    buf = torch.empty(E + 1 + 2 * slots + (nb + 3) // 4, dtype=torch.int32, device=device)
-    offsets, place, order, work = buf.split((E + 1, slots, slots, (nb + 3) // 4))
-    return ExpertRows(offsets, place.view(T, top), order), work, nb
+    nb = _sort_bytes(T, top, E)
+    new = functools.partial(torch.empty, dtype=torch.int32, device=device)
+    return ExpertRows(new(E + 1), new((T, top)), new(T * top)), new((nb + 3) // 4), nb
 
 
 def _expert_rows(rows, dev):

@@ -50,40 +50,30 @@ __device__ __forceinline__ f32x4 mfma_mx4(const uint4& a, const uint4& b, const 
 // ---------------------------------------------------------------------------
 // quantizers
 // ---------------------------------------------------------------------------
-// Eight consecutive values of a lane: 16 bytes of bf16, or 32 of fp32.
+// A lane has 16 bytes of consecutive values: eight bf16, so that four lanes share a block,
+// or four fp32 and eight lanes.
 template <bool kF32>
-struct Eight {
-  uint4 c[kF32 ? 2 : 1];
-};
+constexpr int kValues = kF32 ? 4 : 8;
+template <bool kF32>
+constexpr int kSharers = kBlock / kValues<kF32>;
 
-template <bool kF32, int AUX>
-__device__ __forceinline__ Eight<kF32> load_eight(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
-  Eight<kF32> v;
-  v.c[0] = bload<AUX>(rs, off);
-  if constexpr (kF32) v.c[1] = bload<AUX>(rs, off + 16);
-  return v;
-}
-
-// Exponent field of the largest magnitude of the four lanes' 32 values (255: a NaN or an
-// infinity is among them).
+// Exponent field of the largest magnitude of the block (255: a NaN or an infinity is among
+// its values), from the values of its lanes.
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 template <bool kF32>
-__device__ __forceinline__ uint32_t block_exponent(const Eight<kF32>& v) {
+__device__ __forceinline__ uint32_t block_exponent(const uint4& v) {
   uint32_t m;
   if constexpr (kF32) {
-    m = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      m = max(max(max(m, v.c[i].x & 0x7FFFFFFFu), max(v.c[i].y & 0x7FFFFFFFu, v.c[i].z & 0x7FFFFFFFu)), v.c[i].w & 0x7FFFFFFFu);
-    m >>= 23;
+    m = max(max(v.x & 0x7FFFFFFFu, v.y & 0x7FFFFFFFu), max(v.z & 0x7FFFFFFFu, v.w & 0x7FFFFFFFu)) >> 23;
   } else {
     auto mag = [](uint32_t w) { return __builtin_bit_cast(u16x2, w & 0x7FFF7FFFu); };
-    const u16x2 p = __builtin_elementwise_max(__builtin_elementwise_max(mag(v.c[0].x), mag(v.c[0].y)),
-                                              __builtin_elementwise_max(mag(v.c[0].z), mag(v.c[0].w)));
+    const u16x2 p = __builtin_elementwise_max(__builtin_elementwise_max(mag(v.x), mag(v.y)),
+                                              __builtin_elementwise_max(mag(v.z), mag(v.w)));
     m = (uint32_t)max(p[0], p[1]) >> 7;
   }
   m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true));  // lanes 1, 0, 3, 2 of four
   m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true));  // lanes 2, 3, 0, 1
+  if constexpr (kF32) m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x141, 0xF, 0xF, true));  // eight, mirrored
   return m;
 }
 
@@ -91,72 +81,83 @@ __device__ __forceinline__ uint32_t block_exponent(const Eight<kF32>& v) {
 // 4, the largest of E2M1, and at least 2^-127.
 __device__ __forceinline__ uint32_t scale_of(uint32_t m) { return m == 255 ? kNanScale : m > 2 ? m - 2 : 0; }
 
-// Codes of eight values against a scale byte.  The conversion divides by the power of two,
-// rounds to the nearest code, ties to the even one, and saturates; subnormal values and
-// scales included (compared with the definition for every exponent of the scale).
+// Codes of a lane's values against a scale byte (fp32: 16 bits).  The conversion divides by
+// the power of two, rounds to the nearest code, ties to the even one, and saturates;
+// subnormal values and scales included (compared with the definition for every exponent of
+// the scale).
 template <bool kF32>
-__device__ __forceinline__ uint32_t encode_eight(const Eight<kF32>& v, uint32_t s) {
+__device__ __forceinline__ uint32_t encode(const uint4& v, uint32_t s) {
   const float d = __uint_as_float(s << 23);
   uint32_t o = 0;
   if constexpr (kF32) {
     auto f = [](uint32_t u) { return __uint_as_float(u); };
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f(v.c[0].x), f(v.c[0].y), d, 0);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f(v.c[0].z), f(v.c[0].w), d, 1);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f(v.c[1].x), f(v.c[1].y), d, 2);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f(v.c[1].z), f(v.c[1].w), d, 3);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f(v.x), f(v.y), d, 0);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f(v.z), f(v.w), d, 1);
   } else {
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, bitcast<bf16x2>(v.c[0].x), d, 0);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, bitcast<bf16x2>(v.c[0].y), d, 1);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, bitcast<bf16x2>(v.c[0].z), d, 2);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, bitcast<bf16x2>(v.c[0].w), d, 3);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, bitcast<bf16x2>(v.x), d, 0);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, bitcast<bf16x2>(v.y), d, 1);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, bitcast<bf16x2>(v.z), d, 2);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, bitcast<bf16x2>(v.w), d, 3);
   }
   return s == kNanScale ? 0 : o;
 }
 
-// Values of eight codes under a scale byte (255 gives NaN, whatever the code).
+// Values of a lane's codes under a scale byte (255 gives NaN, whatever the code).
 template <bool kF32>
-__device__ __forceinline__ Eight<kF32> decode_eight(uint32_t o, uint32_t s) {
+__device__ __forceinline__ v4u decode(uint32_t o, uint32_t s) {
   const float d = __uint_as_float(s << 23);
-  Eight<kF32> v;
   if constexpr (kF32) {
     const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(o, d, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(o, d, 1);
-    const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(o, d, 2), g = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(o, d, 3);
-    v.c[0] = make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(b[0]), __float_as_uint(b[1]));
-    v.c[1] = make_uint4(__float_as_uint(e[0]), __float_as_uint(e[1]), __float_as_uint(g[0]), __float_as_uint(g[1]));
+    return v4u{__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(b[0]), __float_as_uint(b[1])};
   } else {
-    v.c[0] = make_uint4(bitcast<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o, d, 0)),
-                        bitcast<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o, d, 1)),
-                        bitcast<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o, d, 2)),
-                        bitcast<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o, d, 3)));
+    return v4u{bitcast<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o, d, 0)),
+               bitcast<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o, d, 1)),
+               bitcast<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o, d, 2)),
+               bitcast<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o, d, 3))};
   }
-  return v;
 }
 
 // Activations: rows, codes and scales are all in memory order, so the matrix is one
-// run of blocks whatever its shape.  A wavefront takes 2048 values, four times eight
-// per lane, four lanes to a block.
+// run of blocks whatever its shape.  A wavefront takes 2048 values, 1 KiB per load.
+//
+// Bound by memory: XX.
 template <bool kF32>
 __global__ __launch_bounds__(256) void quantize_tokens_kernel(const uint8_t* __restrict__ x, int64_t values,
                                                               uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
-  constexpr int kIn = kF32 ? 4 : 2, kSpan = 2048;
+  constexpr int kIn = kF32 ? 4 : 2, V = kValues<kF32>, kSpan = 2048, kLoads = kSpan / 64 / V;
   const int lane = threadIdx.x & 63;
   const int64_t at = ((int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kSpan;
   if (at >= values) return;
   const int left = (int)min<int64_t>(values - at, kSpan);  // a multiple of 128
   const __amdgpu_buffer_rsrc_t rs = make_rsrc(x + at * kIn, (uint32_t)left * kIn);
-  Eight<kF32> v[4];
+  uint4 v[kLoads];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) v[u] = load_eight<kF32, kNonTemporal>(rs, (uint32_t)(u * 512 + lane * 8) * kIn);
-  uint32_t mine = 0;
+  for (int u = 0; u < kLoads; ++u) v[u] = bload<kNonTemporal>(rs, (uint32_t)(u * 64 + lane) * 16u);
+  uint32_t mine = 0, o[kLoads];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
+  for (int u = 0; u < kLoads; ++u) {
     const uint32_t s = scale_of(block_exponent<kF32>(v[u]));
-    if ((lane & 3) == u) mine = s;
-    if (u * 512 + lane * 8 < left)
-      *reinterpret_cast<uint32_t*>(q + (at + u * 512 + lane * 8) / 2) = encode_eight<kF32>(v[u], s);
+    if (lane % kSharers<kF32> == u) mine = s;
+    o[u] = encode<kF32>(v[u], s);
   }
-  // lane 4 b + u has the scale of block b of part u
-  const int b = (lane & 3) * 16 + (lane >> 2);
+  uint32_t* to = reinterpret_cast<uint32_t*>(q + at / 2);
+  if constexpr (kF32) {
+    // of two loads, an even lane stores its pair's codes of the first, an odd one those of the second
+#pragma unroll
+    for (int u = 0; u < kLoads; u += 2) {
+      const bool odd = lane & 1;
+      const uint32_t give = odd ? o[u] : o[u + 1], keep = odd ? o[u + 1] : o[u];
+      const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0xB1, 0xF, 0xF, true);  // lanes 1, 0, 3, 2
+      const int i = (u + odd) * 32 + lane / 2;
+      if (i * 8 < left) to[i] = odd ? got | keep << 16 : keep | got << 16;
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u)
+      if ((u * 64 + lane) * V < left) to[u * 64 + lane] = o[u];
+  }
+  // lane kSharers b + u has the scale of block b of load u
+  const int b = lane % kSharers<kF32> * (64 / kSharers<kF32>) + lane / kSharers<kF32>;
   if (b * kBlock < left) scales[at / kBlock + b] = (uint8_t)mine;
 }
 
@@ -164,117 +165,110 @@ template <bool kF32>
 __global__ __launch_bounds__(256) void dequantize_tokens_kernel(const uint8_t* __restrict__ q,
                                                                 const uint8_t* __restrict__ scales, int64_t values,
                                                                 uint8_t* __restrict__ x) {
-  constexpr int kOut = kF32 ? 4 : 2, kSpan = 2048;
+  constexpr int kOut = kF32 ? 4 : 2, V = kValues<kF32>, kSpan = 2048, kLoads = kSpan / 64 / V;
   const int lane = threadIdx.x & 63;
   const int64_t at = ((int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kSpan;
   if (at >= values) return;
   const int left = (int)min<int64_t>(values - at, kSpan);
-  uint32_t o[4], s[4];
+  uint32_t o[kLoads], s[kLoads];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int i = u * 512 + lane * 8;
-    o[u] = i < left ? *reinterpret_cast<const uint32_t*>(q + (at + i) / 2) : 0;
+  for (int u = 0; u < kLoads; ++u) {
+    const int i = (u * 64 + lane) * V;
+    if constexpr (kF32) o[u] = i < left ? *reinterpret_cast<const uint16_t*>(q + (at + i) / 2) : 0;
+    else o[u] = i < left ? *reinterpret_cast<const uint32_t*>(q + (at + i) / 2) : 0;
     s[u] = i < left ? scales[(at + i) / kBlock] : 0;
   }
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int i = u * 512 + lane * 8;
-    if (i >= left) continue;
-    const Eight<kF32> v = decode_eight<kF32>(o[u], s[u]);
-    uint4* to = reinterpret_cast<uint4*>(x + (at + i) * kOut);
-    to[0] = v.c[0];
-    if constexpr (kF32) to[1] = v.c[1];
+  for (int u = 0; u < kLoads; ++u) {
+    const int i = (u * 64 + lane) * V;
+    if (i < left) __builtin_nontemporal_store(decode<kF32>(o[u], s[u]), reinterpret_cast<v4u*>(x + (at + i) * kOut));
   }
 }
 
-// Where a wavefront that goes through 16 rows x 512 inputs finds what lane l holds in
-// load (i, u): row 4 i + l / 16, inputs 128 u + 8 (l % 16) .. + 7, the dword l % 4 of
-// the 16 bytes of block 4 u + (l % 16) / 4.
-struct NativeAt {
-  uint32_t code;   // byte offset in the 4 KiB of codes
-  uint32_t scale;  // byte offset in the 256 bytes of scales
+// Weights: a block of four wavefronts takes 16 rows x 512 inputs, each wavefront whole lines
+// of four rows; the codes change between the two orders in LDS, 16 runs of 256 bytes (one
+// quarter of the lanes in one of the four tiles) 272 bytes apart, which spreads a row's blocks
+// over the banks.
+struct NativeBlock {
+  uint32_t code, scale;  // byte offsets in LDS of block b (0 .. 15) of row `row`
 };
-__device__ __forceinline__ NativeAt native_at(int lane, int i, int u) {
-  const int row = 4 * i + (lane >> 4), b = 4 * u + ((lane & 15) >> 2);
+constexpr int kRunLds = 256 + 16;
+__device__ __forceinline__ NativeBlock native_block(int row, int b) {
   const int half = b >> 3, quarter = (b & 7) >> 1, t = b & 1;
-  return {(uint32_t)((2 * half + t) * 1024 + (quarter * 16 + row) * 16 + (lane & 3) * 4),
-          (uint32_t)((quarter * 16 + row) * 4 + 2 * half + t)};
+  return {(uint32_t)(((2 * half + t) * 4 + quarter) * kRunLds + row * 16), (uint32_t)((quarter * 16 + row) * 4 + 2 * half + t)};
 }
 
-// Weights: a wavefront takes 16 rows x 512 inputs, reads whole lines of a row and
-// writes 64-byte runs of its tiles.  Padding (rows N .., inputs K ..) reads zeros, which
-// give codes and scales of zero.
+// Padding (rows N .., inputs K ..) reads zeros, which give codes and scales of zero.
+//
+// Bound by memory: XX.
 template <bool kF32>
 __global__ __launch_bounds__(256) void quantize_weights_kernel(const uint8_t* __restrict__ W, int64_t N, int K, int words,
-                                                               int64_t items, uint8_t* __restrict__ q,
-                                                               uint8_t* __restrict__ scales) {
-  constexpr int kIn = kF32 ? 4 : 2;
-  const int lane = threadIdx.x & 63;
-  const int64_t item = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (item >= items) return;
-  const int64_t r = item / words;
+                                                               uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
+  constexpr int kIn = kF32 ? 4 : 2, V = kValues<kF32>, kParts = kWord / 64 / V;
+  __shared__ __attribute__((aligned(16))) uint8_t codes[16 * kRunLds], scale[256];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t item = blockIdx.x, r = item / words;
   const int c = (int)(item - r * words);
   const int rows = (int)min<int64_t>(N - r * kTileRows, kTileRows);
   const __amdgpu_buffer_rsrc_t rs = make_rsrc(W + r * kTileRows * K * kIn, (uint32_t)rows * (uint32_t)K * kIn);
+  const int left = K - c * kWord;  // inputs of this word's 512 that there are
+  uint4 v[4][kParts];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      const int k = (p * 64 + lane) * V;
+      v[i][p] = bload<kNonTemporal>(rs, k < left ? ((uint32_t)(4 * wave + i) * (uint32_t)K + (uint32_t)(c * kWord + k)) * kIn : kOob);
+    }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      const NativeBlock at = native_block(4 * wave + i, (p * 64 + lane) / kSharers<kF32>);
+      const uint32_t s = scale_of(block_exponent<kF32>(v[i][p])), o = encode<kF32>(v[i][p], s);
+      const int part = lane % kSharers<kF32>;
+      if constexpr (kF32) *reinterpret_cast<uint16_t*>(codes + at.code + 2 * part) = (uint16_t)o;
+      else *reinterpret_cast<uint32_t*>(codes + at.code + 4 * part) = o;
+      if (part == 0) scale[at.scale] = (uint8_t)s;
+    }
+  __syncthreads();
   const int pairs = (K + kPair - 1) / kPair;
-  uint8_t* qt = q + (r * pairs + 2 * c) * 2048;
-  uint8_t* st = scales + (r * words + c) * 256;
-  const int left = K - c * kWord;              // inputs of this word's 512 that there are
-  const int padded = (pairs - 2 * c) * kPair;  // and with the padding of their codes
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t row = (uint32_t)(4 * i + (lane >> 4));
-    Eight<kF32> v[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int k = 128 * u + 8 * (lane & 15);
-      v[u] = load_eight<kF32, 0>(rs, k < left ? (row * (uint32_t)K + (uint32_t)(c * kWord + k)) * kIn : kOob);
-    }
-    uint32_t mine = 0;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t s = scale_of(block_exponent<kF32>(v[u]));
-      if ((lane & 3) == u) mine = s;
-      if (128 * u + 8 * (lane & 15) < padded)
-        *reinterpret_cast<uint32_t*>(qt + native_at(lane, i, u).code) = encode_eight<kF32>(v[u], s);
-    }
-    st[native_at(lane, i, lane & 3).scale] = (uint8_t)mine;
-  }
+  if ((int)(threadIdx.x >> 7) < pairs - 2 * c)  // (two tiles for each 256 inputs)
+    reinterpret_cast<uint4*>(q + (r * pairs + 2 * c) * 2048)[threadIdx.x] =
+        *reinterpret_cast<const uint4*>(codes + (threadIdx.x >> 4) * kRunLds + (threadIdx.x & 15) * 16);
+  if (threadIdx.x < 16)
+    reinterpret_cast<uint4*>(scales + (r * words + c) * 256)[threadIdx.x] = reinterpret_cast<const uint4*>(scale)[threadIdx.x];
 }
 
 template <bool kF32>
 __global__ __launch_bounds__(256) void dequantize_weights_kernel(const uint8_t* __restrict__ q,
                                                                  const uint8_t* __restrict__ scales, int64_t N, int K,
-                                                                 int words, int64_t items, uint8_t* __restrict__ W) {
-  constexpr int kOut = kF32 ? 4 : 2;
-  const int lane = threadIdx.x & 63;
-  const int64_t item = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (item >= items) return;
-  const int64_t r = item / words;
+                                                                 int words, uint8_t* __restrict__ W) {
+  constexpr int kOut = kF32 ? 4 : 2, V = kValues<kF32>, kParts = kWord / 64 / V;
+  __shared__ __attribute__((aligned(16))) uint8_t codes[16 * kRunLds], scale[256];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t item = blockIdx.x, r = item / words;
   const int c = (int)(item - r * words);
   const int pairs = (K + kPair - 1) / kPair;
-  const uint8_t* qt = q + (r * pairs + 2 * c) * 2048;
-  const uint8_t* st = scales + (r * words + c) * 256;
+  if ((int)(threadIdx.x >> 7) < pairs - 2 * c)
+    *reinterpret_cast<uint4*>(codes + (threadIdx.x >> 4) * kRunLds + (threadIdx.x & 15) * 16) =
+        reinterpret_cast<const uint4*>(q + (r * pairs + 2 * c) * 2048)[threadIdx.x];
+  if (threadIdx.x < 16)
+    reinterpret_cast<uint4*>(scale)[threadIdx.x] = reinterpret_cast<const uint4*>(scales + (r * words + c) * 256)[threadIdx.x];
+  __syncthreads();
   const int left = K - c * kWord;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t n = r * kTileRows + 4 * i + (lane >> 4);
-    uint32_t o[4], s[4];
+    const int64_t n = r * kTileRows + 4 * wave + i;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const NativeAt at = native_at(lane, i, u);
-      const bool there = n < N && 128 * u + 8 * (lane & 15) < left;
-      o[u] = there ? *reinterpret_cast<const uint32_t*>(qt + at.code) : 0;
-      s[u] = there ? st[at.scale] : 0;
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int k = 128 * u + 8 * (lane & 15);
+    for (int p = 0; p < kParts; ++p) {
+      const int k = (p * 64 + lane) * V, part = lane % kSharers<kF32>;
       if (n >= N || k >= left) continue;
-      const Eight<kF32> v = decode_eight<kF32>(o[u], s[u]);
-      uint4* to = reinterpret_cast<uint4*>(W + (n * K + c * kWord + k) * kOut);
-      to[0] = v.c[0];
-      if constexpr (kF32) to[1] = v.c[1];
+      const NativeBlock at = native_block(4 * wave + i, (p * 64 + lane) / kSharers<kF32>);
+      uint32_t o;
+      if constexpr (kF32) o = *reinterpret_cast<const uint16_t*>(codes + at.code + 2 * part);
+      else o = *reinterpret_cast<const uint32_t*>(codes + at.code + 4 * part);
+      __builtin_nontemporal_store(decode<kF32>(o, scale[at.scale]), reinterpret_cast<v4u*>(W + (n * K + c * kWord + k) * kOut));
     }
   }
 }
@@ -981,26 +975,26 @@ hipError_t in_launches(int64_t items, int64_t most, Launch launch) {
 
 hipError_t launch_quantize_mx4(const void* W, bool f32, int64_t N, int64_t K, uint8_t* q, uint8_t* s, hipStream_t st) {
   const int64_t words = (K + kWord - 1) / kWord, pairs = (K + kPair - 1) / kPair, es = f32 ? 4 : 2;
-  return in_launches((N + kTileRows - 1) / kTileRows, kMostWaves / words, [&](int64_t r, int64_t n) {
+  return in_launches((N + kTileRows - 1) / kTileRows, kMostWaves / 4 / words, [&](int64_t r, int64_t n) {
     const uint8_t* from = static_cast<const uint8_t*>(W) + r * kTileRows * K * es;
-    const int64_t items = n * words, rows = N - r * kTileRows;
+    const int64_t rows = N - r * kTileRows;
     uint8_t *qt = q + r * pairs * 2048, *sc = s + r * words * 256;
-    const unsigned blocks = (unsigned)((items + 3) / 4);
-    if (f32) quantize_weights_kernel<true><<<blocks, 256, 0, st>>>(from, rows, (int)K, (int)words, items, qt, sc);
-    else quantize_weights_kernel<false><<<blocks, 256, 0, st>>>(from, rows, (int)K, (int)words, items, qt, sc);
+    const unsigned blocks = (unsigned)(n * words);
+    if (f32) quantize_weights_kernel<true><<<blocks, 256, 0, st>>>(from, rows, (int)K, (int)words, qt, sc);
+    else quantize_weights_kernel<false><<<blocks, 256, 0, st>>>(from, rows, (int)K, (int)words, qt, sc);
   });
 }
 
 hipError_t launch_dequantize_mx4(const uint8_t* q, const uint8_t* s, int64_t N, int64_t K, void* W, bool f32,
                                  hipStream_t st) {
   const int64_t words = (K + kWord - 1) / kWord, pairs = (K + kPair - 1) / kPair, es = f32 ? 4 : 2;
-  return in_launches((N + kTileRows - 1) / kTileRows, kMostWaves / words, [&](int64_t r, int64_t n) {
+  return in_launches((N + kTileRows - 1) / kTileRows, kMostWaves / 4 / words, [&](int64_t r, int64_t n) {
     uint8_t* to = static_cast<uint8_t*>(W) + r * kTileRows * K * es;
-    const int64_t items = n * words, rows = N - r * kTileRows;
+    const int64_t rows = N - r * kTileRows;
     const uint8_t *qt = q + r * pairs * 2048, *sc = s + r * words * 256;
-    const unsigned blocks = (unsigned)((items + 3) / 4);
-    if (f32) dequantize_weights_kernel<true><<<blocks, 256, 0, st>>>(qt, sc, rows, (int)K, (int)words, items, to);
-    else dequantize_weights_kernel<false><<<blocks, 256, 0, st>>>(qt, sc, rows, (int)K, (int)words, items, to);
+    const unsigned blocks = (unsigned)(n * words);
+    if (f32) dequantize_weights_kernel<true><<<blocks, 256, 0, st>>>(qt, sc, rows, (int)K, (int)words, to);
+    else dequantize_weights_kernel<false><<<blocks, 256, 0, st>>>(qt, sc, rows, (int)K, (int)words, to);
   });
 }
 
