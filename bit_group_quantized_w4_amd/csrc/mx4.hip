@@ -317,6 +317,7 @@ struct MxArgs {
   const uint8_t* s;
   void* y;
   int M, K, N, experts;
+  bool lines;  // rows of y are whole lines of memory
 };
 
 template <bool kF32>
@@ -445,18 +446,23 @@ __global__ __launch_bounds__(NW * 64) void mx4_stream_kernel(const MxArgs a) {
 }
 
 // Sums of TM row tiles of a wavefront, lane l's outputs n0 + 16 (l / 16) .. + 15 of rows
-// m0 + l % 16 + 16 i, stored by way of `stage` (kStageBytes of the wavefront's own).
+// m0 + l % 16 + 16 i, stored by way of `stage` (kStageBytes of the wavefront's own).  Past the
+// caches where that writes whole lines, which leaves the L2 to x and the weights (us through
+// the caches and past them: 8190 rows of 9216 x 2560 123 and 110, 4096 of 17408 x 5120 194 and 187; but 4096 of
+// 9217 x 2560, whose rows end inside a line, 70 and 86).
 template <int TM, bool kF32>
-__device__ __forceinline__ void store_tile(const MxArgs& a, const RowTile& rt, int m0, int n0,
-                                           const f32x4 (&acc)[TM][4], uint8_t* stage) {
+__device__ __forceinline__ void store_tile(const MxArgs& a, const RowTile& rt, int m0, int n0, const f32x4 (&acc)[TM][4],
+                                           uint8_t* stage) {
   uint32_t* words = reinterpret_cast<uint32_t*>(stage);
   const int lane = threadIdx.x & 63;
+  auto value = [](uint32_t w, int, int) { return __uint_as_float(w); };
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       *reinterpret_cast<f32x4*>(words + (lane & 15) * kStagePitch + 16 * (lane >> 4) + 4 * j) = acc[i][j];
-    store_stage<kF32>(words, a.y, a.N, m0 + 16 * i, rt.r1, n0, [](uint32_t w, int, int) { return __uint_as_float(w); });
+    if (a.lines) store_stage<kF32, true>(words, a.y, a.N, m0 + 16 * i, rt.r1, n0, value);
+    else store_stage<kF32>(words, a.y, a.N, m0 + 16 * i, rt.r1, n0, value);
   }
 }
 
@@ -1043,7 +1049,8 @@ bool fits_linear_mx4(int64_t M, int64_t N, int64_t K, int64_t experts, bool grou
 hipError_t launch_linear_mx4(const uint8_t* xq, const uint8_t* xs, int64_t M, int64_t K, const int32_t* offsets,
                              int64_t experts, const uint8_t* q, const uint8_t* s, int64_t N, void* y, bool f32,
                              hipStream_t st) {
-  const MxArgs a{xq, xs, offsets, q, s, y, (int)M, (int)K, (int)N, (int)experts};
+  const bool lines = N * (f32 ? 4 : 2) % 128 == 0 && reinterpret_cast<uintptr_t>(y) % 128 == 0;
+  const MxArgs a{xq, xs, offsets, q, s, y, (int)M, (int)K, (int)N, (int)experts, lines};
   return f32 ? launch_product<true>(a, st) : launch_product<false>(a, st);
 }
 

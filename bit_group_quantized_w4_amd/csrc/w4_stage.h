@@ -15,6 +15,8 @@ namespace w4 {
 // (The pitch of 68 words spreads sixteen rows over the banks.)
 constexpr int kStagePitch = 68, kStageBytes = 16 * kStagePitch * 4;
 
+typedef uint32_t piece_at_any __attribute__((ext_vector_type(4), aligned(1)));
+
 // Stores rows m0 .. m0 + 15 below m1, outputs n0 .. n0 + 63 below N: value(word, s, e) of the
 // staged words is the output of row m0 + stage_row(s) and column n0 + stage_col() + e.
 template <bool kF32>
@@ -27,7 +29,8 @@ template <bool kF32>
 __device__ __forceinline__ int stage_row(int s) {
   return kStageOut<kF32> * s + (threadIdx.x & 63) / (64 / kStageOut<kF32>);
 }
-template <bool kF32, class Value>
+// kPast: whole pieces are stored past the caches.
+template <bool kF32, bool kPast = false, class Value>
 __device__ __forceinline__ void store_stage(const uint32_t* stage, void* y, int N, int m0, int m1, int n0, Value value) {
   constexpr int E = kStageOut<kF32>;
   // the stage is this wavefront's own, and its LDS operations run in order
@@ -52,7 +55,11 @@ __device__ __forceinline__ void store_stage(const uint32_t* stage, void* y, int 
     if constexpr (kF32) {
       float* to = static_cast<float*>(y) + at;
       if (count == E) {
-        __builtin_memcpy(to, v, 16);
+        if constexpr (kPast)
+          __builtin_nontemporal_store(
+              piece_at_any{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])},
+              reinterpret_cast<piece_at_any*>(to));
+        else __builtin_memcpy(to, v, 16);
       } else {
 #pragma unroll
         for (int e = 0; e < E; ++e)
@@ -64,7 +71,8 @@ __device__ __forceinline__ void store_stage(const uint32_t* stage, void* y, int 
 #pragma unroll
       for (int e = 0; e < E / 2; ++e) u[e] = f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
       if (count == E) {
-        __builtin_memcpy(to, u, 16);
+        if constexpr (kPast) __builtin_nontemporal_store(piece_at_any{u[0], u[1], u[2], u[3]}, reinterpret_cast<piece_at_any*>(to));
+        else __builtin_memcpy(to, u, 16);
       } else {
 #pragma unroll
         for (int e = 0; e < E; ++e)
