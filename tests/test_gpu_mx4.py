@@ -419,3 +419,93 @@ def test_refusals_on_the_gpu(w4, gpu):
     assert w4.linear_mx4(u8(0, 64), u8(0, 4), q, s, 16).shape == (0, 16)
     assert w4.linear_mx4(u8(2, 64), u8(2, 4), u8(0), u8(0), 0).shape == (2, 0)
     assert w4.quantize_tokens_mx4(torch.zeros((0, 128), device=gpu))[0].shape == (0, 64)
+
+
+# ----------------------------------------------------------------------------
+# larger sizes, which reach every kernel: against float64 on the GPU
+# ----------------------------------------------------------------------------
+
+def _draw(gpu, seed, rows, K, spread=6):
+    g = torch.Generator(device=gpu)
+    g.manual_seed(seed)
+    codes = torch.randint(0, 256, (rows, K // 2), generator=g, device=gpu, dtype=torch.int32).to(torch.uint8)
+    return codes, torch.randint(127 - spread, 128 + spread, (rows, K // 32), generator=g, device=gpu).to(torch.uint8)
+
+
+def _values(codes, scales):
+    """float64 values, by the table of E2M1."""
+    grid = torch.tensor(list(oracle.E2M1) + [-v for v in oracle.E2M1], dtype=torch.float64, device=codes.device)
+    v = torch.stack((grid[(codes & 15).int()], grid[(codes >> 4).int()]), -1).reshape(codes.shape[0], -1, 32)
+    return (v * torch.exp2(scales.double() - 127)[..., None]).reshape(codes.shape[0], -1)
+
+
+def _check_on_gpu(y32, x, w, K, what):
+    ref, absdot = x @ w.t().contiguous(), x.abs() @ w.abs().t().contiguous()
+    off = (y32.double() - ref).abs() - oracle.mx4_tolerance(absdot, K)
+    assert bool((off <= 0).all()), f"{what}: {int((off > 0).sum())} of {off.numel()} out of tolerance"
+
+
+@pytest.mark.parametrize("M,N,K", [
+    (16, 2000, 4736), (9, 5000, 1152), (3, 9216, 2560), (13, 20000, 640),  # streamed: 1, 2 row blocks; 4, 2, 1 wavefronts
+    (333, 1000, 640), (130, 520, 2560),                                    # streamed, many row tiles
+    (33, 5000, 4736), (64, 5000, 1408),                                    # 32 x 64
+    (333, 3000, 384), (300, 5000, 2560),                                   # 64 x 64
+    (512, 2560, 9216),                                                     # 64 x 128
+    (512, 9000, 1152), (2000, 3001, 1152),                                 # 128 x 128
+    (1200, 2561, 1408),                                                    # 256 x 256, every tile cut
+    (2100, 2561, 640), (3900, 5000, 1152), (2048, 9216, 128),              # whole and low ones; and cut ones
+    (4096, 2048, 1408),                                                    # rows of whole lines
+])
+def test_linear_mx4_every_kernel(w4, gpu, M, N, K):
+    _say(f"linear_mx4 {M} rows of {N}x{K}")
+    wq, ws = _draw(gpu, M + N, N, K)
+    xq, xs = _draw(gpu, K, M, K)
+    q, s = w4.pack_mx4(wq, ws)
+    buf = torch.full((M + 2, N), 77.0, device=gpu)
+    y32 = w4.linear_mx4(xq, xs, q, s, N, out=buf[1:1 + M])
+    assert _frame_kept(buf)
+    _check_on_gpu(y32, _values(xq, xs), _values(wq, ws), K, "fp32")
+    buf16, y16 = _framed(gpu, M, N, BF16)
+    w4.linear_mx4(xq, xs, q, s, N, out=y16)
+    assert _frame_kept(buf16) and torch.equal(y16, y32.to(BF16))
+
+
+@pytest.mark.parametrize("sizes,N,K", [([700, 0, 1030, 257, 90], 2100, 640), ([3, 20, 41, 0, 64, 33, 17, 9], 1500, 1152),
+                                       ([200, 100, 150, 130], 3000, 1408), ([1500, 1, 1300, 2], 1280, 896),
+                                       ([20, 12, 0, 15, 9, 30, 17], 5000, 384)])
+def test_grouped_linear_mx4_larger(w4, gpu, sizes, N, K):
+    _say(f"grouped_linear_mx4 {sizes} {N}x{K}")
+    E, first, after = len(sizes), 5, 3
+    M = first + sum(sizes) + after
+    offsets = torch.tensor([first] + [first + sum(sizes[:e + 1]) for e in range(E)], dtype=torch.int32, device=gpu)
+    made = [_draw(gpu, 10 + e, N, K) for e in range(E)]
+    packed = [w4.pack_mx4(*m) for m in made]
+    q, s = torch.stack([p[0] for p in packed]), torch.stack([p[1] for p in packed])
+    xq, xs = _draw(gpu, 9, M, K)
+    buf = torch.full((M + 2, N), 77.0, device=gpu)
+    y32 = w4.grouped_linear_mx4(xq, xs, offsets, q, s, N, out=buf[1:1 + M])
+    assert _frame_kept(buf) and bool((y32[:first] == 77).all()) and bool((y32[M - after:] == 77).all())
+    x = _values(xq, xs)
+    at = first
+    for e in range(E):
+        if sizes[e]:
+            _check_on_gpu(y32[at:at + sizes[e]], x[at:at + sizes[e]], _values(*made[e]), K, f"expert {e}")
+        at += sizes[e]
+    y16 = w4.grouped_linear_mx4(xq, xs, offsets, q, s, N)
+    assert torch.equal(y16[first:M - after], y32[first:M - after].to(BF16))
+
+
+def test_next_rows_do_not_matter(w4, gpu):
+    """Where K ends inside 512 inputs, what follows a row of x (the next row: NaN scales, infinities' codes) and
+    what follows the last one must not reach it."""
+    _say("linear_mx4 rows beside rows of NaN")
+    for K in (128, 384, 640, 1152, 1408):
+        for M, N in ((16, 300), (40, 5000), (130, 5000), (600, 9000), (1500, 3000)):
+            wq, ws = _draw(gpu, 1, N, K)
+            xq, xs = _draw(gpu, 2, M, K)
+            q, s = w4.pack_mx4(wq, ws)
+            want = w4.linear_mx4(xq, xs, q, s, N)
+            xs2 = xs.clone()
+            xs2[1::2] = 255
+            got = w4.linear_mx4(xq, xs2, q, s, N)
+            assert torch.equal(got[0::2], want[0::2]) and bool(got[1::2].isnan().all()), (K, M, N)
