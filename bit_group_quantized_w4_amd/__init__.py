@@ -997,10 +997,14 @@ def _sort_bytes(T, top, E):
 
 
 def _empty_rows(T, top, E, device):
-    """(ExpertRows to be filled, workspace, its bytes)."""
-    nb = _sort_bytes(T, top, E)
-    new = functools.partial(torch.empty, dtype=torch.int32, device=device)
-    return ExpertRows(new(E + 1), new((T, top)), new(T * top)), new((nb + 3) // 4), nb
+    """(ExpertRows to be filled, address of a workspace or None, its bytes, what holds it)."""
+    slots, nb = T * top, _sort_bytes(T, top, E)
+    offsets, place, order = torch.empty(E + 1 + 2 * slots, dtype=torch.int32, device=device).split((E + 1, slots, slots))
+    rows = ExpertRows(offsets, place.view(T, top), order)
+    if not nb:
+        return rows, None, 0, None
+    work = torch.empty(nb, dtype=torch.uint8, device=device)
+    return rows, work.data_ptr(), nb, work
 
 
 def _expert_rows(rows, dev):
@@ -1021,9 +1025,9 @@ def expert_sort(experts, E):
     [0, E) being of no expert (their slots are dropped).  Returns ExpertRows, whose offsets the grouped linears
     take.  Slots of one expert keep their order."""
     dev, T, top, size = _ids(experts, E)
-    rows, work, nb = _empty_rows(T, top, E, experts.device)
+    rows, work, nb, _held = _empty_rows(T, top, E, experts.device)
     _launch("w4_expert_sort", dev, experts.data_ptr(), size, T, top, E, rows.offsets.data_ptr(), rows.place.data_ptr(),
-            rows.order.data_ptr(), work.data_ptr(), nb)
+            rows.order.data_ptr(), work, nb)
     return rows
 
 
@@ -1140,11 +1144,11 @@ def _dispatch(x, experts, E):
         raise ValueError(f"experts: tensors on several devices ({experts.device} and {x.device})")
     if x.shape[0] != T:
         raise ValueError(f"x must have {T} rows (got {x.shape[0]})")
-    rows, work, nb = _empty_rows(T, top, E, x.device)
+    rows, work, nb, _held = _empty_rows(T, top, E, x.device)
     xs = torch.empty((T * top,) + x.shape[1:], dtype=x.dtype, device=x.device)
     width = x.element_size() * (x.shape[1] if x.dim() == 2 else 1)
     _launch("w4_expert_dispatch", dev, x.data_ptr(), width, experts.data_ptr(), size, T, top, E, rows.offsets.data_ptr(),
-            rows.place.data_ptr(), rows.order.data_ptr(), xs.data_ptr(), work.data_ptr(), nb)
+            rows.place.data_ptr(), rows.order.data_ptr(), xs.data_ptr(), work, nb)
     return xs, rows
 
 

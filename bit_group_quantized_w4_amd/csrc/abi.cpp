@@ -385,11 +385,12 @@ w4_status check_sort(const void* experts, int id_bytes, int64_t tokens, int64_t 
   if (!slots_ok(tokens, top) || !experts_ok(count)) return W4_ERR_SHAPE;
   if (id_bytes != 4 && id_bytes != 8) return W4_ERR_ARG;
   const int64_t slots = tokens * top;
-  if (!offsets || (slots && (!experts || !place || !order)) || !workspace) return W4_ERR_NULL;
+  const size_t need = w4_expert_sort_workspace_bytes(tokens, top, count);
+  if (!offsets || (slots && (!experts || !place || !order)) || (need && !workspace)) return W4_ERR_NULL;
   if (!aligned(experts, id_bytes) || !aligned(offsets, 4) || !aligned(place, 4) || !aligned(order, 4) ||
       !aligned(workspace, 4))
     return W4_ERR_ALIGN;
-  if (workspace_bytes < w4_expert_sort_workspace_bytes(tokens, top, count)) return W4_ERR_ARG;
+  if (need && workspace_bytes < need) return W4_ERR_ARG;
   const Span out[] = {{offsets, 4 * ((size_t)count + 1)}, {place, 4 * (size_t)slots}, {order, 4 * (size_t)slots},
                       {workspace, workspace_bytes}};
   const Span in[] = {{experts, (size_t)id_bytes * slots}};

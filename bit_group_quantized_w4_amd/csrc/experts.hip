@@ -555,7 +555,7 @@ hipError_t launch_sort(const Id* ids, int64_t tokens, int64_t top, int64_t exper
 }  // namespace
 
 size_t expert_sort_workspace(int64_t tokens, int64_t top, int64_t experts) {
-  return few_slots(tokens, top) ? sizeof(int) : (size_t)sort_blocks(tokens * top) * (size_t)(experts + 1) * sizeof(int);
+  return few_slots(tokens, top) ? 0 : (size_t)sort_blocks(tokens * top) * (size_t)(experts + 1) * sizeof(int);
 }
 
 hipError_t launch_expert_dispatch(const void* x, int64_t bytes, const void* ids, bool wide, int64_t tokens, int64_t top,

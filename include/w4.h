@@ -833,7 +833,8 @@ w4_status w4_linear_grouped_mx4_f32(const uint8_t* xq, const uint8_t* xs, int64_
  *                  offsets[experts] on.
  *   workspace      device memory of w4_expert_sort_workspace_bytes(tokens, top, experts)
  *                  bytes, 4-byte aligned; overwritten, of no meaning between calls.
- *                  Calls that overlap in time need one each.
+ *                  Calls that overlap in time need one each.  Few slots need none (0 bytes:
+ *                  NULL will do; the function gives 0 for shapes that are refused, too).
  * Index buffers are 4-byte aligned (ids by id_bytes).  Rows may start anywhere that
  * their type may (row_bytes: anywhere).  Outputs overlap no
  * input and no other output (W4_ERR_ARG).  The calls below take offsets and place as

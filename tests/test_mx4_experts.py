@@ -237,15 +237,15 @@ def test_linear_mx4_of_too_many_threads_is_refused(w4):
 
 def test_expert_sort_refusals(w4):
     lib = w4.library()
-    need = lib.w4_expert_sort_workspace_bytes(10, 2, 8)
-    assert need >= 4 and need % 4 == 0
-    assert lib.w4_expert_sort_workspace_bytes(10000, 2, 8) >= 9 * 4  # the counts of a block at least
+    assert lib.w4_expert_sort_workspace_bytes(10, 2, 8) == 0  # few slots
+    need = lib.w4_expert_sort_workspace_bytes(10000, 2, 8)
+    assert need >= 9 * 4 and need % 4 == 0  # the counts of a block at least
     for T, top, E in ((-1, 2, 8), (10, 0, 8), (262140, 2, 8), (131071, 3, 8), (10, 2, 4097), (10, 2, -1)):
         assert lib.w4_expert_sort_workspace_bytes(T, top, E) == 0
     ids, off, place, order, ws = (FAKE + i * MiB for i in range(5))
 
     def call(**kw):
-        a = dict(ids=ids, size=8, T=10, top=2, E=8, off=off, place=place, order=order, ws=ws, n=need)
+        a = dict(ids=ids, size=8, T=10000, top=2, E=8, off=off, place=place, order=order, ws=ws, n=need)
         a.update(kw)
         return lib.w4_expert_sort(a["ids"], a["size"], a["T"], a["top"], a["E"], a["off"], a["place"], a["order"],
                                   a["ws"], a["n"], None)
@@ -258,7 +258,8 @@ def test_expert_sort_refusals(w4):
         assert call(**bad) == ERR_NULL, bad
     for bad in (dict(ids=ids + 4), dict(off=off + 2), dict(place=place + 1), dict(order=order + 2), dict(ws=ws + 2)):
         assert call(**bad) == ERR_ALIGN, bad
-    for bad in (dict(off=ids + 152), dict(place=off + 32), dict(order=place + 76), dict(ws=order + 76),
+    assert call(T=10, ws=None, off=None) == ERR_NULL
+    for bad in (dict(off=ids + 159992), dict(place=off + 32), dict(order=place + 79996), dict(ws=order + 79996),
                 dict(ws=ids - need + 4)):
         assert call(**bad) == ERR_ARG, bad
     assert call(ids=ids + 4, size=4, off=None) == ERR_NULL  # 4-byte ids need 4
@@ -278,15 +279,15 @@ def test_expert_row_refusals(w4):
         assert take(**bad) == ERR_ARG, bad
     assert take(T=0, x=None, xs=None) == OK and take(n=0, x=None, xs=None) == OK
 
-    ws, need = FAKE + 9 * MiB, lib.w4_expert_sort_workspace_bytes(10, 2, 8)
+    ws, need = FAKE + 9 * MiB, lib.w4_expert_sort_workspace_bytes(10000, 2, 8)
     ids, order = FAKE + 10 * MiB, FAKE + 11 * MiB
-    dispatch = lambda x=x, n=64, ids=ids, size=8, T=10, xs=xs, ws=ws, nb=need: (  # noqa: E731
+    dispatch = lambda x=x, n=10, ids=ids, size=8, T=10000, xs=xs, ws=ws, nb=need: (  # noqa: E731
         lib.w4_expert_dispatch(x, n, ids, size, T, 2, 8, off, place, order, xs, ws, nb, None))
     assert dispatch(n=-1) == ERR_SHAPE and dispatch(T=-1) == ERR_SHAPE and dispatch(size=3) == ERR_ARG
     assert dispatch(x=None) == ERR_NULL and dispatch(xs=None) == ERR_NULL and dispatch(ids=None) == ERR_NULL
     assert dispatch(nb=need - 1) == ERR_ARG and dispatch(ids=ids + 4) == ERR_ALIGN
-    for bad in (dict(xs=x + 639), dict(xs=off + 32), dict(xs=place + 76), dict(xs=order + 76), dict(xs=ws + 4),
-                dict(xs=ids + 156), dict(ws=x + 636)):
+    for bad in (dict(xs=x + 99999), dict(xs=off + 32), dict(xs=place + 79996), dict(xs=order + 79996), dict(xs=ws + 4),
+                dict(xs=ids + 159996), dict(ws=x + 99996)):
         assert dispatch(**bad) == ERR_ARG, bad
 
     for yt in (0, 1):
