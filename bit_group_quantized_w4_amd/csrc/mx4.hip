@@ -607,8 +607,8 @@ __device__ __forceinline__ void all_done() {
 // beside the first two parts, as one load holds up the wavefront while the address unit of
 // the CU takes it.  kAhead: a share of the lines that the step after next needs is touched
 // early, so that its loads find them in the L2 of the XCD: share `share_x` of eight of
-// the rows and `share_w` of four of the row blocks, as the blocks that run at one time on an XCD
-// hold four row tiles times eight panels (tile_of_block).
+// the rows and `share_w` of four of the row blocks (-1: all of them), as the blocks that run at
+// one time on an XCD hold four row tiles or more times up to eight panels (band_tile).
 template <int WM, int WN, int TM, bool kAhead, bool kF32, int L0, int L1, int LS>
 __device__ __forceinline__ void run_tile(const MxArgs& a, const RowTile& rt, int rb0, int share_x, int share_w,
                                          uint8_t (&lds0)[L0], uint8_t (&lds1)[L1], uint8_t (&scales)[LS],
@@ -623,8 +623,11 @@ __device__ __forceinline__ void run_tile(const MxArgs& a, const RowTile& rt, int
   const __amdgpu_buffer_rsrc_t touch_rs = touch_x ? tw.o.x : tw.o.w;
   const uint32_t touch_at =
       touch_x ? (tw.lane < S::BM / 4 / NW ? (uint32_t)(S::BM / 8 * share_x + S::BM / 4 / NW * tw.wave + tw.lane) * tw.k_half : kOob)
-              : (tw.lane < 16 ? (uint32_t)(rb0 + S::BN / 64 * share_w + tw.wave - NW / 2) * (uint32_t)steps * 2048u + 128u * tw.lane
-                              : kOob);
+      : share_w < 0 ? (uint32_t)(rb0 + S::BN / 64 * (tw.wave - NW / 2) + (tw.lane >> 4)) * (uint32_t)steps * 2048u +
+                          128u * (tw.lane & 15)
+                    : (tw.lane < 16 ? (uint32_t)(rb0 + S::BN / 64 * share_w + tw.wave - NW / 2) * (uint32_t)steps * 2048u +
+                                          128u * tw.lane
+                                    : kOob);
   auto touch = [&](int s) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(touch_rs, (typename TileWave<WM, WN, TM>::lds_ptr)(touched + tw.wave * 256), 4,
                                              (int)(touch_at + ((uint32_t)min(s, steps - 1) << (touch_x ? 7 : 11))), 0, 0, 0);
@@ -750,19 +753,19 @@ __global__ __launch_bounds__(512, 1) void mx4_tile_kernel(const MxArgs a, int pa
     b = total - cut + (i >> 2);
     if (b >= total) return;
   }
-  int t, p;
-  tile_of_block(b, total / panels, panels, t, p);
-  RowTile rt;
-  if (!find_row_tile(a.offsets, a.experts, a.M, 256, t, rt)) return;
+  BandTile bt;
+  if (!band_tile(a.offsets, a.experts, a.M, 256, panels, slot_of_block(b, total), bt)) return;
+  RowTile rt = bt.rt;
+  const int p = bt.p, share_w = bt.height < 4 ? -1 : bt.in & 3;
   if (quarter >= 0) {
     const int rb0 = 16 * p + 8 * (quarter & 1);
     rt.r0 += 128 * (quarter >> 1);
     rt.r1 = min(rt.r1, rt.r0 + 128);
     if (rt.r0 < rt.r1 && rb0 * kTileRows < a.N) run_tile<4, 2, 2, false, kF32>(a, rt, rb0, 0, 0, lds0, lds1, scales, touched);
   } else if (rt.r1 - rt.r0 <= 128) {
-    run_tile<2, 4, 4, true, kF32>(a, rt, 16 * p, p & 7, t & 3, lds0, lds1, scales, touched);
+    run_tile<2, 4, 4, true, kF32>(a, rt, 16 * p, p & 7, share_w, lds0, lds1, scales, touched);
   } else {
-    run_tile<2, 4, 8, true, kF32>(a, rt, 16 * p, p & 7, t & 3, lds0, lds1, scales, touched);
+    run_tile<2, 4, 8, true, kF32>(a, rt, 16 * p, p & 7, share_w, lds0, lds1, scales, touched);
   }
 }
 

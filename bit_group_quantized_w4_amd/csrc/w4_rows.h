@@ -103,6 +103,48 @@ __device__ __forceinline__ void tile_of_block(int b, int tiles, int panels, int&
   t = band * kBand + in - p * height;
 }
 
+// Block b's place in the order of tiles * panels pieces of work, each XCD given a contiguous
+// run of them (as tile_of_block does).
+__device__ __forceinline__ int slot_of_block(int b, int total) {
+  const int xcd = b % kXcds;
+  return xcd * (total / kXcds) + min(xcd, total % kXcds) + b / kXcds;
+}
+
+// Piece of work `at` of tiles * panels: expert by expert, an expert's row tiles in bands of kBand
+// (up to 2 kBand - 1 in the last), panel by panel within a band.  So blocks that run at one
+// time share not only rows and panels but also the expert, whose weights the panels are of
+// (tile_of_block's bands may hold several experts').  Returns whether there is such a piece.
+struct BandTile {
+  RowTile rt;
+  int p;           // panel
+  int in, height;  // of the band: the row tile's place and the number of them
+};
+__device__ __forceinline__ bool band_tile(const int* __restrict__ offsets, int experts, int M, int BM, int panels, int at,
+                                          BandTile& o) {
+  int t = at / panels, first, end, before, n;  // the expert's rows, the tiles before its own, and its own
+  if (!offsets) {
+    o.rt.expert = before = first = 0;
+    end = M;
+    n = (M + BM - 1) / BM;
+    if (t >= n) return false;
+  } else {
+    if (!find_row_tile(offsets, experts, M, BM, t, o.rt)) return false;
+    first = min(max(offsets[o.rt.expert], 0), M);
+    end = min(max(offsets[o.rt.expert + 1], 0), M);
+    n = (end - first + BM - 1) / BM;
+    before = t - (o.rt.r0 - first) / BM;
+  }
+  const int local = at - before * panels, bands = n < kBand ? 1 : n / kBand;
+  const int band = min(local / (kBand * panels), bands - 1), left = local - band * kBand * panels;
+  o.height = band == bands - 1 ? n - band * kBand : kBand;
+  o.p = left / o.height;
+  o.in = left - o.p * o.height;
+  o.rt.r0 = first + (band * kBand + o.in) * BM;
+  o.rt.r1 = min(end, o.rt.r0 + BM);
+  o.rt.alone = n == 1;
+  return true;
+}
+
 // Row tiles a launch has to cover (see above).
 inline int64_t max_row_tiles(int64_t M, int64_t experts, bool grouped, int BM) {
   if (!grouped) return (M + BM - 1) / BM;
