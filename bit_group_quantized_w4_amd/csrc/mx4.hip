@@ -778,12 +778,12 @@ __global__ __launch_bounds__(WM* WN * 64) void mx4_deep_kernel(const MxArgs a, i
   __shared__ __attribute__((aligned(1024))) uint8_t lds0[S::kBuffer], lds1[S::kBuffer], lds2[S::kBuffer], lds3[S::kBuffer],
       scales0[S::kScales], scales2[S::kScales];
   // (offsets whose ranges overlap could make more tiles than the launch covers)
-  const int tiles = min(count_row_tiles(a.offsets, a.experts, a.M, S::BM), (int)gridDim.x / panels);
-  if ((int)blockIdx.x >= tiles * panels) return;
-  int t, p;
-  tile_of_block(blockIdx.x, tiles, panels, t, p);
-  RowTile rt;
-  if (!find_row_tile(a.offsets, a.experts, a.M, S::BM, t, rt)) return;
+  const int total = min(count_row_tiles(a.offsets, a.experts, a.M, S::BM), (int)gridDim.x / panels) * panels;
+  if ((int)blockIdx.x >= total) return;
+  BandTile bt;
+  if (!band_tile(a.offsets, a.experts, a.M, S::BM, panels, slot_of_block(blockIdx.x, total), bt)) return;
+  const RowTile& rt = bt.rt;
+  const int p = bt.p;
   const int rb0 = p * (S::BN / 16);
   const TileWave<WM, WN, TM> tw(a, rt, rb0);
   const int steps = tw.o.pairs;
@@ -883,14 +883,15 @@ struct Mx4Shape {
   int slots;
   double start, one, all;
 };
-// Constants that lose least by the choice over the times of all these kernels on 14 matrices (N from
-// 300 to 28672, K from 128 to 9216) at 17 to 4096 rows, other weights than the last call's: 1.5% on
-// average against the best of them each time, 26% at most.
+// Constants that lose least by the choice over the times of all these kernels (other weights than
+// the last call's) on 14 matrices, N from 300 to 28672 and K from 128 to 9216, at 17 to 3000 rows and on 5
+// sets of 8 to 128 experts at 13 to 400 rows each, popularity as 1 / rank and its root: 2.4% on
+// average against the best of them each time, 30% at most.
 constexpr Mx4Shape kMx4Shapes[] = {
-    {Mx4::kTile256, 256, 256, 512, 256, 3.4, 0, 1.77},      {Mx4::kDeep128, 128, 128, 256, 256, 6.3, 0.48, 0.66},
-    {Mx4::kDeep64x128, 64, 128, 256, 256, 8.9, 0, 0.363},   {Mx4::kDeep64, 64, 64, 256, 512, 3.7, 0.196, 0.666},
-    {Mx4::kDeep32x64, 32, 64, 128, 512, 3.7, 0.173, 0.393}, {Mx4::kStream2x2, 16, 32, 128, 2048, 2.5, 0, 1.76},
-    {Mx4::kStream2x1, 16, 32, 64, 4096, 2.5, 0.234, 2.87},  {Mx4::kStream2x4, 16, 32, 256, 0, 0, 0, 0},
+    {Mx4::kTile256, 256, 256, 512, 256, 3.4, 0, 1.77},    {Mx4::kDeep128, 128, 128, 256, 256, 6.2, 0.473, 0.669},
+    {Mx4::kDeep64x128, 64, 128, 256, 256, 9.7, 0, 0.395}, {Mx4::kDeep64, 64, 64, 256, 512, 3.7, 0.227, 0.669},
+    {Mx4::kDeep32x64, 32, 64, 128, 512, 3.6, 0.2, 0.547}, {Mx4::kStream2x2, 16, 32, 128, 2048, 3.8, 0, 1.33},
+    {Mx4::kStream2x1, 16, 32, 64, 4096, 2.7, 0.343, 1.53}, {Mx4::kStream2x4, 16, 32, 256, 0, 0, 0, 0},
     {Mx4::kStream1x4, 16, 16, 256, 0, 0, 0, 0},
 };
 

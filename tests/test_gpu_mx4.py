@@ -472,7 +472,9 @@ def test_linear_mx4_every_kernel(w4, gpu, M, N, K):
 
 @pytest.mark.parametrize("sizes,N,K", [([700, 0, 1030, 257, 90], 2100, 640), ([3, 20, 41, 0, 64, 33, 17, 9], 1500, 1152),
                                        ([200, 100, 150, 130], 3000, 1408), ([1500, 1, 1300, 2], 1280, 896),
-                                       ([20, 12, 0, 15, 9, 30, 17], 5000, 384)])
+                                       ([20, 12, 0, 15, 9, 30, 17], 5000, 384),
+                                       ([128, 100, 151, 140, 90, 133, 127, 161], 5120, 2560),
+                                       ([31, 50, 0, 7, 40, 32], 5000, 2560)])
 def test_grouped_linear_mx4_larger(w4, gpu, sizes, N, K):
     _say(f"grouped_linear_mx4 {sizes} {N}x{K}")
     E, first, after = len(sizes), 5, 3
