@@ -1081,16 +1081,23 @@ def expert_combine_backward(grad, y, weights, rows, need_y=True, need_weights=Tr
     return dy, dw
 
 
+def _take_gradient(grad, rows):
+    if grad is None:
+        return None
+    return _combine(grad.contiguous(), None, rows, grad.get_device(), None, grad.dtype)
+
+
 class _TakeFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, rows):
         ctx.rows = rows
+        ctx.set_materialize_grads(False)
         return _take(x, rows, x.get_device())
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
-        return _combine(grad.contiguous(), None, ctx.rows, grad.get_device(), None, grad.dtype), None
+        return _take_gradient(grad, ctx.rows), None
 
 
 class _DispatchFunction(torch.autograd.Function):
@@ -1099,12 +1106,13 @@ class _DispatchFunction(torch.autograd.Function):
         xs, rows = _dispatch(x, experts, E)
         ctx.rows = rows
         ctx.mark_non_differentiable(*rows)
+        ctx.set_materialize_grads(False)
         return (xs,) + rows
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad, *_):
-        return _combine(grad.contiguous(), None, ctx.rows, grad.get_device(), None, grad.dtype), None, None
+        return _take_gradient(grad, ctx.rows), None, None
 
 
 class _CombineFunction(torch.autograd.Function):
@@ -1112,11 +1120,14 @@ class _CombineFunction(torch.autograd.Function):
     def forward(ctx, y, weights, rows, out_dtype):
         ctx.save_for_backward(y, weights)
         ctx.rows = rows
+        ctx.set_materialize_grads(False)
         return _combine(y, weights, rows, y.get_device(), None, out_dtype)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
+        if grad is None:
+            return None, None, None, None
         y, weights = ctx.saved_tensors
         return expert_combine_backward(grad.contiguous(), y, weights, ctx.rows, *ctx.needs_input_grad[:2]) + (None, None)
 

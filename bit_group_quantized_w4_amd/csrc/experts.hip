@@ -8,7 +8,8 @@
 //   out[t] = sum_j w[t][j] y[place[t][j]],
 //   dy[place[t][j]] = w[t][j] dout[t],    dw[t][j] = sum_k dout[t][k] y[place[t][j]][k]
 //
-// Sums run in fp32 in a fixed order; nothing is added with atomics but counts.
+// Sums run in fp32 in a fixed order; nothing is added with atomics but counts.  Every kernel
+// moves bytes: what they cannot do without is each row read once and written once.
 #include "w4_device.h"
 #include "w4_launch.h"
 #include "w4_rows.h"
@@ -64,7 +65,7 @@ __global__ __launch_bounds__(256) void expert_count_kernel(const Id* __restrict_
 // a time: the lanes of a wavefront with a slot's key are found by one ballot per bit of
 // the keys, and the wavefronts take their turns at the expert's next row.
 //
-// Bound by latency: 32760 slots of 128 experts take XX us with the counts.
+// Bound by latency: 32760 slots of 128 experts take 10 us, 3 of them the counts; 120000 of 500 23 us.
 template <typename Id>
 __global__ __launch_bounds__(256) void expert_place_kernel(const Id* __restrict__ ids, int slots, int chunk, int experts,
                                                            const int* __restrict__ hist, int* __restrict__ offsets,
@@ -180,7 +181,7 @@ __device__ __forceinline__ void take_piece(const uint8_t* from, int64_t bytes, i
 // A row is read once and written to the rows of its token's slots: `lanes` lanes of a
 // wavefront (a power of two, 64 for long rows) take that many pieces of one token each.
 //
-// Bound by memory, XX.
+// Bound by memory: 4095 rows of 5120 bf16 to eight rows each (377 MB) take 66 us (5.7 TB/s).
 template <bool kUniform, bool kPast>
 __global__ __launch_bounds__(256) void expert_take_kernel(const uint8_t* __restrict__ x, int64_t bytes, int slots, int top,
                                                           const int* __restrict__ valid_at, const int* __restrict__ place,
@@ -351,7 +352,8 @@ __device__ __forceinline__ void load_rows(const void* y, int64_t K, const int (&
 // out[t] = sum_j w[t][j] y[place[t][j]] (w nullptr: ones): `lanes` lanes of a wavefront take
 // that many pieces of one token, eight slots at a time.
 //
-// Bound by memory, XX.
+// Bound by memory: 4095 x 8 rows of 5120 bf16, 1/16 of them dropped (356 MB), take 60 us (5.9 TB/s); 8 tokens
+// of two rows of 2560 3 us, the latency of a place and of its row.
 template <bool kUniform, bool kF32>
 __global__ __launch_bounds__(256) void expert_combine_kernel(const CombineArgs a, int lanes, int chunks, int t0,
                                                              int t1) {
@@ -407,7 +409,7 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(const CombineArgs a
 // token.  They go through its row of dout piece by piece, write w dout to the rows of
 // its slots and add up dout y for each of them, eight slots at a time.  dy or dw may be nullptr.
 //
-// Bound by memory, XX.
+// Bound by memory: the same 4095 x 8 rows (692 MB) take 119 to 140 us (4.9 to 5.8 TB/s).
 template <int W, bool kPast, bool kF32>
 __global__ __launch_bounds__(256) void expert_combine_backward_kernel(const CombineBackwardArgs a, int lanes) {
   constexpr int V = kPer<kF32>;

@@ -120,7 +120,8 @@ __device__ __forceinline__ v4u decode(uint32_t o, uint32_t s) {
 // Activations: rows, codes and scales are all in memory order, so the matrix is one
 // run of blocks whatever its shape.  A wavefront takes 2048 values, 1 KiB per load.
 //
-// Bound by memory: XX.
+// Bound by memory: 4099 x 28672 bf16 (298 MB) take 46 us (6.5 TB/s; a copy reaches 5.1), fp32
+// 86 us (6.2); back to bf16 43 us.
 template <bool kF32>
 __global__ __launch_bounds__(256) void quantize_tokens_kernel(const uint8_t* __restrict__ x, int64_t values,
                                                               uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
@@ -200,7 +201,9 @@ __device__ __forceinline__ NativeBlock native_block(int row, int b) {
 
 // Padding (rows N .., inputs K ..) reads zeros, which give codes and scales of zero.
 //
-// Bound by memory: XX.
+// Bound by memory: 28672 x 8192 fp32 (1.06 GB) take 172 us (6.2 TB/s), bf16 89 (6.7); back to
+// bf16 83 us.  (Codes stored from the lanes that made them, 64 bytes of a tile at a time, and
+// loads through the caches: 217 and 132 us; values stored through the caches 140.)
 template <bool kF32>
 __global__ __launch_bounds__(256) void quantize_weights_kernel(const uint8_t* __restrict__ W, int64_t N, int K, int words,
                                                                uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
@@ -353,6 +356,10 @@ __device__ __forceinline__ Operands operands_of(const MxArgs& a, const RowTile& 
 // rows of x; its NW wavefronts divide K.  Lane l of a wavefront holds row l % 16 of x and of
 // a row block, inputs 64 (l / 16) .. + 63 of 256, and D[4 (l / 16) + j][l % 16], j = 0..3,
 // all straight from memory, D pairs of tiles ahead of the products.
+//
+// Bound by the weight stream: 13 rows of 28672 x 8192 (125 MB) take 22 us (5.8 TB/s); one row of
+// 9216 x 2560 4.8 us, the latency of its loads and of the join over K.  (Three or four pairs ahead
+// leave fewer wavefronts room: 24.0 and 24.2 us.)
 template <int R, int NW, int kCache, bool kF32>
 __device__ __forceinline__ void stream_row_tile(const MxArgs& a, const RowTile& rt, int rb0, f32x4 (&red)[NW][R][64]) {
   constexpr int D = 2;
@@ -433,7 +440,7 @@ __device__ __forceinline__ void stream_row_tile(const MxArgs& a, const RowTile& 
 }
 
 // kPast: an expert's weights are read past the caches, unless another row tile of the
-// expert reads them too.
+// expert reads them too (13 rows of 28672 x 8192 24.6 us past them, 26.8 through them).
 template <int R, int NW, bool kPast, bool kF32>
 __global__ __launch_bounds__(NW * 64) void mx4_stream_kernel(const MxArgs a) {
   const int nb = (a.N + kTileRows - 1) / kTileRows, panels = (nb + R - 1) / R;
@@ -601,14 +608,20 @@ __device__ __forceinline__ void all_done() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// Many rows: two buffers, loads one step ahead.  The products of a step run in four parts
+// Many rows: two buffers, loads one step ahead.  4096 rows of 17408 x 5120 take 178 to 191 us, 3.8 to
+// 4.1 PFLOP/s (a large library product of this format reaches 3.0 on the same card; the matrix
+// units alone, on random codes, 7.0).  The products of a step run in four parts
 // (half of the rows times one of the two products).  Operands are read from LDS one
 // part ahead, beside the products of the part before; the next step's loads are issued
 // beside the first two parts, as one load holds up the wavefront while the address unit of
-// the CU takes it.  kAhead: a share of the lines that the step after next needs is touched
+// the CU takes it (all beside the first part: 237 us, beside two 224).  kAhead: a share of the lines that the step after next needs is touched
 // early, so that its loads find them in the L2 of the XCD: share `share_x` of eight of
 // the rows and `share_w` of four of the row blocks (-1: all of them), as the blocks that run at
-// one time on an XCD hold four row tiles or more times up to eight panels (band_tile).
+// one time on an XCD hold four row tiles or more times up to eight panels (band_tile): 224 and
+// 205 us.  What is left above the matrix units' own time: the loads (without them 171 us, before the
+// last round was cut), reads of scales (8 us) and the last, partial round.  (Four wavefronts of 128 x 128
+// with their sums in the accumulation registers read a third less from LDS, but one wavefront
+// per SIMD hides nothing: 306 us.)
 template <int WM, int WN, int TM, bool kAhead, bool kF32, int L0, int L1, int LS>
 __device__ __forceinline__ void run_tile(const MxArgs& a, const RowTile& rt, int rb0, int share_x, int share_w,
                                          uint8_t (&lds0)[L0], uint8_t (&lds1)[L1], uint8_t (&scales)[LS],
@@ -731,8 +744,10 @@ __device__ __forceinline__ void run_tile(const MxArgs& a, const RowTile& rt, int
 
 // 256 x 256 per block of eight wavefronts, one block per CU.  What is left of the tiles
 // after whole rounds of kCus, if at most a quarter of a round, is cut into four tiles of 128 x
-// 128 each, which fill another round in less than half the time of whole tiles; a tile
-// of at most 128 rows (an expert's last) is half as high.
+// 128 each, which fill another round in less than half the time of whole tiles (us whole and
+// cut: 2048 rows of 9216 x 2560 44 and 34, 4096 of 17408 x 5120 206 and 195); a tile of at most 128 rows (an
+// expert's last) is half as high.  (Blocks that go from tile to tile, the next one's first loads
+// issued before the outputs are stored, took 1 to 4% longer.)
 constexpr int kCus = 256, kMostCut = kCus / 4;
 
 template <bool kF32>
@@ -770,7 +785,10 @@ __global__ __launch_bounds__(512, 1) void mx4_tile_kernel(const MxArgs a, int pa
 }
 
 // Fewer rows, where each block's time is the latency of its loads: smaller tiles, four
-// buffers, loads three steps ahead, two parts (one product each) per step.
+// buffers, loads three steps ahead, two parts (one product each) per step.  333 rows of 2561 x 9216
+// take 11.5 us as 64 x 64 (37 streamed, 20 as 128 x 128 of this form, 33 as 256 x 256): 246 blocks
+// load 145 MB through the L2s, 13 TB/s.  (Two buffers 20 us; two groups of wavefronts that divide
+// K 13 us; two wavefronts of 32 rows per block instead of four of 16 12.7.)
 template <int WM, int WN, int TM, bool kF32>
 __global__ __launch_bounds__(WM* WN * 64) void mx4_deep_kernel(const MxArgs a, int panels) {
   using S = TileShape<WM, WN, TM>;

@@ -405,3 +405,32 @@ def test_refusals_on_the_gpu(w4, gpu):
     dy, dw = w4.expert_combine_backward(torch.zeros((4, 0), device=gpu), torch.zeros((8, 0), device=gpu),
                                         torch.ones((4, 2), device=gpu), rows)
     assert dy.shape == (8, 0) and not bool(dw.any())
+
+
+def test_capture_of_a_backward_pass(w4, gpu):
+    """Forward and backward of dispatch and combine in one graph, replayed with other values between."""
+    _say("captured backward pass")
+    rng = np.random.default_rng(15)
+    T, top, E, K = 50, 2, 6, 136
+    ids = torch.from_numpy(_ids(rng, T, top, E, "dropped")).to(gpu)
+
+    def step(x, w, dout):
+        xs, rows = w4.expert_dispatch(x, ids, E)
+        return torch.autograd.grad(w4.expert_combine(xs * 2.0, w, rows), (x, w), dout)
+
+    values = [(torch.randn((T, K), device=gpu), torch.rand((T, top), device=gpu), torch.randn((T, K), device=gpu))
+              for _ in range(3)]
+    want = [[g.clone() for g in step(x.clone().requires_grad_(), w.clone().requires_grad_(), d)] for x, w, d in values]
+    x, w, d = (v.clone() for v in values[0])
+    xg, wg = x.requires_grad_(), w.requires_grad_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(xg, wg, d)
+    for turn in range(6):
+        k = turn % 3
+        with torch.no_grad():
+            xg.copy_(values[k][0]), wg.copy_(values[k][1]), d.copy_(values[k][2])
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, want[k]):
+            assert torch.equal(a, b)
