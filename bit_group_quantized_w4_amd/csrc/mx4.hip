@@ -980,7 +980,15 @@ hipError_t launch_product(const MxArgs& a, hipStream_t st) {
     case Mx4::kStream1x4: mx4_stream_kernel<1, 4, false, kF32><<<blocks, 256, 0, st>>>(a); break;
     case Mx4::kStream2x4: mx4_stream_kernel<2, 4, false, kF32><<<blocks, 256, 0, st>>>(a); break;
     case Mx4::kStream2x2: mx4_stream_kernel<2, 2, false, kF32><<<blocks, 128, 0, st>>>(a); break;
-    case Mx4::kStream2x1: mx4_stream_kernel<2, 1, true, kF32><<<blocks, 64, 0, st>>>(a); break;
+    case Mx4::kStream2x1: {
+      // Past the caches from 40 MB of weights that the call can read (us through the caches and past
+      // them: one row of 17408 x 5120, 45 MB, 11.2 and 10.5; 8 rows of 8 experts of 9216 x 2560 18.3 and
+      // 16.2; but 2 rows of these 6.2 and 6.9, 16 of 128 of 1408 x 2560, 29 MB, 6.3 and 6.9).
+      const int64_t bytes = (a.experts < a.M ? a.experts : a.M) * (int64_t)a.N * a.K / 2;
+      if (bytes >= (int64_t)40 << 20) mx4_stream_kernel<2, 1, true, kF32><<<blocks, 64, 0, st>>>(a);
+      else mx4_stream_kernel<2, 1, false, kF32><<<blocks, 64, 0, st>>>(a);
+      break;
+    }
   }
   return hipGetLastError();
 }
