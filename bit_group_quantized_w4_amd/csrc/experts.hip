@@ -476,6 +476,10 @@ __global__ __launch_bounds__(256) void expert_combine_backward_kernel(const Comb
       }
     }
     if (!a.dw) continue;
+    // (an infinity or NaN of dout times the zeros of a dropped slot is NaN: its sum is zero all the same)
+#pragma unroll
+    for (int j = 0; j < kRowsAtOnce; ++j)
+      if (row[j] < 0) sum[j] = 0.0f;
 #pragma unroll
     for (int j = 0; j < kRowsAtOnce; ++j)
       for (int d = min(span, 64) / 2; d; d >>= 1) sum[j] += __shfl_xor(sum[j], d);

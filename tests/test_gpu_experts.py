@@ -434,3 +434,21 @@ def test_capture_of_a_backward_pass(w4, gpu):
         torch.cuda.synchronize()
         for a, b in zip(out, want[k]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,top,E,K", [(9, 3, 5, 7), (9, 3, 5, 77), (40, 4, 16, 264), (300, 10, 16, 1027), (1100, 2, 16, 1024)])
+@pytest.mark.parametrize("yt", [BF16, F32])
+def test_gradients_of_infinite_outputs(w4, gpu, T, top, E, K, yt):
+    """Dropped slots have zeros as gradients of their weights, whatever the gradient of the output holds."""
+    rng = np.random.default_rng(T + K)
+    _say(f"gradients of infinite outputs {T} x {top} of {E}, {K}")
+    ids = _ids(rng, T, top, E, "dropped")
+    rows, y, w = _combine_inputs(rng, gpu, T, top, E, K, yt, F32, "dropped")
+    g = torch.from_numpy(rng.standard_normal((T, K)).astype(np.float32))
+    g[::3, K // 2] = float("inf")
+    g[1::3, K - 1] = float("nan")
+    dy, dw = w4.expert_combine_backward(g.to(gpu), y.to(gpu), w.to(gpu), rows)
+    place, n = rows.place.cpu().numpy(), int(rows.offsets[E])
+    assert (place < 0).any() and (dw.cpu().numpy()[place < 0] == 0).all()
+    assert not np.isfinite(dw.cpu().numpy()[:2][place[:2] >= 0]).any()
+    assert (dy[n:] == 0).all()
