@@ -45,8 +45,6 @@ __device__ __forceinline__ void scan_counts(int* count, int n, int* wave_sum) {
   }
 }
 
-constexpr int kMostBlocks = 128;
-
 // Counts of each block's `chunk` slots by expert: hist[block][experts + 1].
 template <typename Id>
 __global__ __launch_bounds__(256) void expert_count_kernel(const Id* __restrict__ ids, int slots, int chunk, int experts,
@@ -65,7 +63,7 @@ __global__ __launch_bounds__(256) void expert_count_kernel(const Id* __restrict_
 // a time: the lanes of a wavefront with a slot's key are found by one ballot per bit of
 // the keys, and the wavefronts take their turns at the expert's next row.
 //
-// Bound by latency: 32760 slots of 128 experts take 10 us, 3 of them the counts; 120000 of 500 23 us.
+// Bound by latency: 32760 slots of 128 experts take 9 us, 3 of them the counts; 120000 of 500 21 us.
 template <typename Id>
 __global__ __launch_bounds__(256) void expert_place_kernel(const Id* __restrict__ ids, int slots, int chunk, int experts,
                                                            const int* __restrict__ hist, int* __restrict__ offsets,
@@ -208,7 +206,7 @@ __global__ __launch_bounds__(256) void expert_take_kernel(const uint8_t* __restr
 // slot's key in LDS; a slot's row is the number of slots that come before it, by expert and
 // then by index, which 256 threads count with ballots.  The offsets (the number of keys below
 // each) are shared out over the blocks.  `bytes` 0: no rows.
-constexpr int kFewSlots = 2048, kMostTop = 64;
+constexpr int kFewSlots = 2048, kMostTop = 64, kFewCounts = 8192;
 
 template <typename Id>
 __global__ __launch_bounds__(256) void expert_dispatch_kernel(const uint8_t* __restrict__ x, int64_t bytes,
@@ -503,10 +501,12 @@ __global__ __launch_bounds__(256) void expert_combine_backward_kernel(const Comb
   }
 }
 
-// Slots per block of the sort: at least 512, at most kMostBlocks blocks.
+// Slots per block of the sort: 64 blocks, and 128 from 2048 slots in each on, as every block
+// reads the counts of all (us: 8192 slots of 128 experts 7.7 by 256, 8.6 by 512 and 10.6 by 1024; 32760
+// 10.3, 9.1 and 10.8; 120000 of 500 21.0 by 2048, 22.3 by 1024; 262136 of 128 24.7 by 4096, 18.0 by 2048).
 int sort_chunk(int64_t slots) {
-  const int64_t per = (slots + kMostBlocks - 1) / kMostBlocks;
-  return (int)((per < 512 ? 512 : per) + 255) / 256 * 256;
+  const int64_t per = (slots + 63) / 64;
+  return (int)((per < 1 ? 1 : per <= 2048 ? per : (per + 1) / 2) + 255) / 256 * 256;
 }
 int sort_blocks(int64_t slots) {
   const int chunk = sort_chunk(slots);
@@ -514,10 +514,18 @@ int sort_blocks(int64_t slots) {
   return n < 1 ? 1 : (int)n;
 }
 
-// Whether a call is one launch: blocks count every slot once per slot of their own.
-bool few_slots(int64_t tokens, int64_t top) { return tokens * top <= kFewSlots && top <= kMostTop; }
+// Whether a call is one launch: its blocks count every slot once per slot of their own (us, the
+// sort alone and with rows of 2560 bf16, in one launch and in several: 16 x 8 slots 3.9 and 5.7, 6.5
+// and 8.5; 128 x 8 7.6 and 8.1, 10.5 and 11.3; 2048 x 1 8.1 and 7.5, 11.2 and 11.7; but 256 x 8 12.0
+// and 8.5, 15.8 and 11.9).
+bool few_slots(int64_t tokens, int64_t top) {
+  return tokens * top <= kFewSlots && top <= kMostTop && tokens * top * top <= kFewCounts;
+}
 
 // Lanes of a wavefront that share a row of `pieces` pieces, and how many times they need to.
+// (us, take, combine and its gradients of 32768 tokens to four rows each, and with a wavefront for
+// every row: rows of 32 bf16 4.1, 3.7 and 8.2, and 9.5, 16.6 and 59.8; of 128 8.3, 7.2 and 25.5, and 9.0, 16.9
+// and 69.2; of 256 14.5, 14.7 and 45.2, and 12.6, 17.5 and 75.5.)
 struct Lanes {
   int lanes, chunks;
 };

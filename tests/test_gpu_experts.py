@@ -62,7 +62,7 @@ def _check_rows(rows, ids, E):
     return place
 
 
-SORTS = [(0, 2, 8), (1, 1, 1), (1, 8, 128), (8, 2, 64), (5, 3, 0), (77, 3, 7), (64, 4, 300), (128, 8, 64), (300, 6, 4096),
+SORTS = [(0, 2, 8), (0, 100, 8), (1, 65, 300), (2, 64, 64), (2, 65, 64), (128, 8, 9), (129, 8, 9), (16384, 8, 128), (16385, 8, 128), (1, 1, 1), (1, 8, 128), (8, 2, 64), (5, 3, 0), (77, 3, 7), (64, 4, 300), (128, 8, 64), (300, 6, 4096),
          (333, 1, 5), (1111, 2, 33), (4095, 8, 128), (32768, 1, 2), (32767, 8, 256), (87380, 3, 4096)]
 
 
