@@ -608,18 +608,20 @@ __device__ __forceinline__ void all_done() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// Many rows: two buffers, loads one step ahead.  4096 rows of 17408 x 5120 take 178 to 191 us, 3.8 to
+// Many rows: two buffers, loads one step ahead.  4096 rows of 17408 x 5120 take 178 to 190 us, 3.8 to
 // 4.1 PFLOP/s (a large library product of this format reaches 3.0 on the same card; the matrix
 // units alone, on random codes, 7.0).  The products of a step run in four parts
 // (half of the rows times one of the two products).  Operands are read from LDS one
-// part ahead, beside the products of the part before; the next step's loads are issued
-// beside the first two parts, as one load holds up the wavefront while the address unit of
-// the CU takes it (all beside the first part: 237 us, beside two 224).  kAhead: a share of the lines that the step after next needs is touched
+// part ahead, beside the products of the part before.  The next step's loads are issued one by one in
+// the first two parts, as one load holds up the wavefront while the address unit of
+// the CU takes it (all beside the first part 237 us, beside two 224), each behind a product,
+// which runs meanwhile (8190 rows of 9216 x 2560 110.3 us ahead of the products, 108.7 behind).  kAhead: a
+// share of the lines that the step after next needs is touched
 // early, so that its loads find them in the L2 of the XCD: share `share_x` of eight of
 // the rows and `share_w` of four of the row blocks (-1: all of them), as the blocks that run at
 // one time on an XCD hold four row tiles or more times up to eight panels (band_tile): 224 and
-// 205 us.  What is left above the matrix units' own time: the loads (without them 171 us, before the
-// last round was cut), reads of scales (8 us) and the last, partial round.  (Four wavefronts of 128 x 128
+// 205 us.  What is left above the matrix units' own time: the loads (without them 171 us where it took
+// 237), reads of scales (8 us) and the last, partial round.  (Four wavefronts of 128 x 128
 // with their sums in the accumulation registers read a third less from LDS, but one wavefront
 // per SIMD hides nothing: 306 us.)
 template <int WM, int WN, int TM, bool kAhead, bool kF32, int L0, int L1, int LS>
@@ -653,16 +655,23 @@ __device__ __forceinline__ void run_tile(const MxArgs& a, const RowTile& rt, int
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
   uint4 x[2][TH], w[2][TN];  // x by row half, w by product
   uint32_t sx[2][TH], sx_read[TH][2], sw[TN], sw_read[TN];
-  // the products t of row half c of a step of parity P; beside(i) comes before row tile i's
-  auto multiply = [&](auto parity, auto product, int c, auto beside) {
+  // the products t of row half c of a step of parity P; beside(i) comes before row tile i's, after(i)
+  // behind the first of them
+  auto multiply = [&](auto parity, auto product, int c, auto beside, auto after) {
     constexpr int t = decltype(product)::value, kByte = 2 * decltype(parity)::value + t;
 #pragma unroll
     for (int i = 0; i < TH; ++i) {
       beside(i);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
+      for (int j = 0; j < TN; ++j) {
         acc[c * TH + i][j] = mfma_mx4<kByte, kByte>(w[t][j], x[c][i], acc[c * TH + i][j], sw[j], sx[c][i]);
+        if (j == 0) {
+          __builtin_amdgcn_sched_barrier(0);
+          after(i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -684,14 +693,15 @@ __device__ __forceinline__ void run_tile(const MxArgs& a, const RowTile& rt, int
     };
     all_done<kAhead ? 1 : 0>();  // `cur` is filled, and nothing reads `nxt` any more
     multiply(other, One(), 1, [&](int i) {
-      load(0, i);
-      if (!even && i == 0) tw.load_scales(s + 1, scales);
       read(0, i);
       if constexpr (even) {
         tw.read_xs(i, scales, sx_read[i]);
 #pragma unroll
         for (int j = i * TN / TH; j < (i + 1) * TN / TH; ++j) sw_read[j] = tw.read_ws(j, scales);
       }
+    }, [&](int i) {
+      load(0, i);
+      if (!even && i == 0) tw.load_scales(s + 1, scales);
     });
     operands_ready();
     if constexpr (even) {
@@ -701,21 +711,21 @@ __device__ __forceinline__ void run_tile(const MxArgs& a, const RowTile& rt, int
       for (int j = 0; j < TN; ++j) sw[j] = sw_read[j];
     }
     multiply(parity, Zero(), 0, [&](int i) {
-      load(1, i);
       x[1][i] = tw.read_x(0, TH + i, cur);
       if constexpr (even) tw.read_xs(TH + i, scales, sx_read[i]);
-    });
+    }, [&](int i) { load(1, i); });
     operands_ready();
     if constexpr (even) {
 #pragma unroll
       for (int i = 0; i < TH; ++i) sx[1][i] = tw.take_xs(s, sx_read[i]);
     }
     multiply(parity, Zero(), 1, [&](int i) {
-      if (kAhead && i == 0) touch(s + 2);  // the last of the step: what all_done leaves in flight
       read(1, i);
+    }, [&](int i) {
+      if (kAhead && i == 0) touch(s + 2);  // the last of the step: what all_done leaves in flight
     });
     operands_ready();
-    multiply(parity, One(), 0, [&](int i) { x[1][i] = tw.read_x(1, TH + i, cur); });
+    multiply(parity, One(), 0, [&](int i) { x[1][i] = tw.read_x(1, TH + i, cur); }, [](int) {});
   };
 
 #pragma unroll
@@ -736,7 +746,7 @@ __device__ __forceinline__ void run_tile(const MxArgs& a, const RowTile& rt, int
     step(Zero(), One(), s, lds0, lds1);
     step(One(), Zero(), s + 1, lds1, lds0);
   }
-  multiply(One(), One(), 1, [](int) {});
+  multiply(One(), One(), 1, [](int) {}, [](int) {});
   all_done<0>();  // no load into LDS is left, and nothing reads what the stages overwrite
   static_assert(NW * kStageBytes <= L0, "stages fit a buffer");
   store_tile<TM, kF32>(a, rt, rt.r0 + 16 * tw.wm * TM, 16 * rb0 + 64 * tw.wn, acc, lds0 + tw.wave * kStageBytes);
@@ -784,11 +794,17 @@ __global__ __launch_bounds__(512, 1) void mx4_tile_kernel(const MxArgs a, int pa
   }
 }
 
-// Fewer rows, where each block's time is the latency of its loads: smaller tiles, four
-// buffers, loads three steps ahead, two parts (one product each) per step.  333 rows of 2561 x 9216
-// take 11.5 us as 64 x 64 (37 streamed, 20 as 128 x 128 of this form, 33 as 256 x 256): 246 blocks
-// load 145 MB through the L2s, 13 TB/s.  (Two buffers 20 us; two groups of wavefronts that divide
-// K 13 us; two wavefronts of 32 rows per block instead of four of 16 12.7.)
+// Fewer rows: smaller tiles, four buffers, loads three steps ahead, two parts (one product each)
+// per step; a load is issued behind a product, which runs meanwhile (64 rows of 2561 x 9216 9.4 us ahead
+// of the products, 8.9 behind).  333 rows of 2561 x 9216 take 11.2 us as 64 x 64 (37 streamed, 19 as 128 x 128 of
+// this form, 33 as 256 x 256).
+//
+// Bound by the rate at which a CU loads into LDS, 18 KB of a step in 0.2 us: the loads alone, without
+// products and reads of LDS, take 11.0 of the 11.2 us; the rest alone 8.1, an empty loop 4.0; 41 blocks
+// (64 rows) take no less than 246.  Six or eight buffers change nothing (11.5 and 12.8, with the steps past the
+// last); two 20 us.  (Two wavefronts for each tile twice as high, one product of a step each, read
+// 24 KB of LDS instead of 40, and take 11.9 with the join; groups of wavefronts that divide the steps 13;
+// operands straight to registers, K divided among the wavefronts, 20.)
 template <int WM, int WN, int TM, bool kF32>
 __global__ __launch_bounds__(WM* WN * 64) void mx4_deep_kernel(const MxArgs a, int panels) {
   using S = TileShape<WM, WN, TM>;
@@ -813,15 +829,20 @@ __global__ __launch_bounds__(WM* WN * 64) void mx4_deep_kernel(const MxArgs a, i
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
   uint4 x[2][TM], w[2][TN];  // by product
   uint32_t sx[TM], sx_read[TM][2], sw[TN], sw_read[TN];
-  auto multiply = [&](auto parity, auto product, auto beside) {
+  // the products q of a step of parity P; before(i) comes ahead of row tile i's, after(m) behind product m
+  auto multiply = [&](auto parity, auto product, auto before, auto after) {
     constexpr int q = decltype(product)::value, kByte = 2 * decltype(parity)::value + q;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      beside(i);
+      before(i);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < TN; ++j) acc[i][j] = mfma_mx4<kByte, kByte>(w[q][j], x[q][i], acc[i][j], sw[j], sx[i]);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < TN; ++j) {
+        acc[i][j] = mfma_mx4<kByte, kByte>(w[q][j], x[q][i], acc[i][j], sw[j], sx[i]);
+        __builtin_amdgcn_sched_barrier(0);
+        after(i * TN + j);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   };
   // A step of parity P: `far` is loaded for step s + 3 (with scales, where that is even).
@@ -836,17 +857,20 @@ __global__ __launch_bounds__(WM* WN * 64) void mx4_deep_kernel(const MxArgs a, i
       }
     };
     all_done<2 * kLoads + S::kSl>();  // all but the loads of the next two steps
-    multiply(other, One(), [&](int i) {
+    multiply(
+        other, One(),
+        [&](int i) {
+          read(0, i);
+          if constexpr (even) {
+            tw.read_xs(i, cur_scales, sx_read[i]);
 #pragma unroll
-      for (int l = i * kLoads / TM; l < (i + 1) * kLoads / TM; ++l) tw.load(l, s + 3, far);
-      if (!even && i == TM - 1) tw.load_scales(s + 3, far_scales);
-      read(0, i);
-      if constexpr (even) {
-        tw.read_xs(i, cur_scales, sx_read[i]);
+            for (int j = i * TN / TM; j < (i + 1) * TN / TM; ++j) sw_read[j] = tw.read_ws(j, cur_scales);
+          }
+        },
+        [&](int m) {
 #pragma unroll
-        for (int j = i * TN / TM; j < (i + 1) * TN / TM; ++j) sw_read[j] = tw.read_ws(j, cur_scales);
-      }
-    });
+          for (int l = m * kLoads / (TM * TN); l < (m + 1) * kLoads / (TM * TN); ++l) tw.load(l, s + 3, far);
+        });
     operands_ready();
     if constexpr (even) {
 #pragma unroll
@@ -854,7 +878,10 @@ __global__ __launch_bounds__(WM* WN * 64) void mx4_deep_kernel(const MxArgs a, i
 #pragma unroll
       for (int j = 0; j < TN; ++j) sw[j] = sw_read[j];
     }
-    multiply(parity, Zero(), [&](int i) { read(1, i); });
+    multiply(parity, Zero(), [&](int i) { read(1, i); },
+             [&](int m) {
+               if (!even && m == TM * TN - 1) tw.load_scales(s + 3, far_scales);
+             });
   };
 #pragma unroll
   for (int j = 0; j < TN; ++j) {  // no step before the first
@@ -882,7 +909,7 @@ __global__ __launch_bounds__(WM* WN * 64) void mx4_deep_kernel(const MxArgs a, i
     step(One(), Zero(), s + 3, lds3, lds2, nullptr, scales2);
   }
   operands_ready();
-  multiply(One(), One(), [](int) {});
+  multiply(One(), One(), [](int) {}, [](int) {});
   all_done<0>();  // no load into LDS is left, and nothing reads what the stages overwrite
   static_assert((S::NW + 1) / 2 * kStageBytes <= S::kBuffer, "stages fit two buffers");
   store_tile<TM, kF32>(a, rt, rt.r0 + 16 * tw.wm * TM, 16 * rb0 + 64 * tw.wn, acc,
