@@ -608,8 +608,8 @@ __device__ __forceinline__ void all_done() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// Many rows: two buffers, loads one step ahead.  4096 rows of 17408 x 5120 take 178 to 190 us, 3.8 to
-// 4.1 PFLOP/s (a large library product of this format reaches 3.0 on the same card; the matrix
+// Many rows: two buffers, loads one step ahead.  4096 rows of 17408 x 5120 take 172 to 188 us, 3.9 to
+// 4.2 PFLOP/s (a large library product of this format reaches 3.0 on the same card; the matrix
 // units alone, on random codes, 7.0).  The products of a step run in four parts
 // (half of the rows times one of the two products).  Operands are read from LDS one
 // part ahead, beside the products of the part before.  The next step's loads are issued one by one in
@@ -930,8 +930,9 @@ struct Mx4Shape {
 };
 // Constants that lose least by the choice over the times of all these kernels (other weights than
 // the last call's) on 14 matrices, N from 300 to 28672 and K from 128 to 9216, at 17 to 3000 rows and on 5
-// sets of 8 to 128 experts at 13 to 400 rows each, popularity as 1 / rank and its root: 2.4% on
-// average against the best of them each time, 30% at most.
+// sets of 8 to 128 experts at 13 to 400 rows each, popularity as 1 / rank and its root: 2.5% on
+// average against the best of them each time, 32% at most.  (Constants fitted to one half of the
+// sizes lose 2.6 to 3.5% on the other, and so do rounds of blocks counted as whole.)
 constexpr Mx4Shape kMx4Shapes[] = {
     {Mx4::kTile256, 256, 256, 512, 256, 3.4, 0, 1.77},    {Mx4::kDeep128, 128, 128, 256, 256, 6.2, 0.473, 0.669},
     {Mx4::kDeep64x128, 64, 128, 256, 256, 9.7, 0, 0.395}, {Mx4::kDeep64, 64, 64, 256, 512, 3.7, 0.227, 0.669},
@@ -946,8 +947,8 @@ constexpr Mx4Shape kMx4Shapes[] = {
 // one row block and four wavefronts 4.6, as two and four 5.1, two and two 6.1, two and
 // one 13; 5120 x 5120 5.5, 4.8, 4.7, 8.3; 9216 x 2560 5.3, 5.5, 4.8, 5.5; 13 rows of 28672 x 8192
 // 32.4, 29.0, 26.8, 23.1).  Beyond that the smallest estimate.  512 rows: 2560 x 9216 take 14.6 us as
-// 64 x 128 (160 blocks), 18.5 as 64 x 64, 19.2 as 128 x 128 and 33 as 256 x 256 (20 blocks);
-// 17408 x 5120 60, 58, 52 and 41 us.
+// 64 x 128 (160 blocks), 18.4 as 64 x 64, 19.1 as 128 x 128 and 31 as 256 x 256 (20 blocks);
+// 17408 x 5120 45, 47, 40 and 35 us.
 Mx4 choose_mx4(int64_t M, int64_t N, int64_t K, int64_t experts) {
   const int64_t busy = experts < M ? experts : M, rows = (M + busy - 1) / busy;
   const int64_t nb = (N + kTileRows - 1) / kTileRows * busy, steps = (K + kPair - 1) / kPair;
