@@ -111,9 +111,13 @@ __global__ __launch_bounds__(256) void expert_place_kernel(const Id* __restrict_
     const int rank = __popcll(same & ((1ull << lane) - 1)), n = __popcll(same);
     int row = 0;
     for (int w = 0; w < 4; ++w) {
-      if (w == wave && key >= 0) {
-        row = next[key] + rank;
-        if (rank == n - 1) next[key] = row + 1;  // (after every lane of the wavefront has read it)
+      if (w == wave) {
+        if (key >= 0) row = next[key] + rank;
+        // one lane of each key writes what the others have read: the fence and the barrier hold the
+        // compiler to that order, the LDS runs a wavefront's operations in it
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (key >= 0 && rank == n - 1) next[key] = row + 1;
       }
       __syncthreads();
     }
