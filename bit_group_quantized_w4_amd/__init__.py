@@ -998,9 +998,11 @@ def _sort_bytes(T, top, E):
 
 def _empty_rows(T, top, E, device):
     """(ExpertRows to be filled, address of a workspace or None, its bytes, what holds it)."""
-    slots, nb = T * top, _sort_bytes(T, top, E)
-    offsets, place, order = torch.empty(E + 1 + 2 * slots, dtype=torch.int32, device=device).split((E + 1, slots, slots))
-    rows = ExpertRows(offsets, place.view(T, top), order)
+    nb = _sort_bytes(T, top, E)
+    # (buffers of their own, not parts of one: autograd counts the writes of each by itself)
+    rows = ExpertRows(torch.empty(E + 1, dtype=torch.int32, device=device),
+                      torch.empty((T, top), dtype=torch.int32, device=device),
+                      torch.empty(T * top, dtype=torch.int32, device=device))
     if not nb:
         return rows, None, 0, None
     work = torch.empty(nb, dtype=torch.uint8, device=device)
@@ -1052,13 +1054,17 @@ def _weights(weights, dev, T, top):
 
 
 def _combine(y, weights, rows, dev, out, out_dtype):
-    T, top, E = _expert_rows(rows, dev)
+    T, top, _ = _expert_rows(rows, dev)
     if y.shape[0] != T * top:
         raise ValueError(f"y must have {T * top} rows (got {y.shape[0]})")
-    K = y.shape[1]
+    return _combine_places(y, weights, rows.place, dev, out, out_dtype)
+
+
+def _combine_places(y, weights, place, dev, out, out_dtype):
+    (T, top), K = place.shape, y.shape[1]
     o, _ = _output(out, out_dtype, T, K, y.device)
     w, wt = _weights(weights, dev, T, top)
-    _launch("w4_expert_combine", dev, y.data_ptr(), _TYPES[y.dtype], w, wt, T, top, K, rows.place.data_ptr(),
+    _launch("w4_expert_combine", dev, y.data_ptr(), _TYPES[y.dtype], w, wt, T, top, K, place.data_ptr(),
             _ptr(o, o.dtype, dev, "out", (T, K)), _TYPES[o.dtype])
     return o
 
@@ -1072,39 +1078,50 @@ def expert_combine_backward(grad, y, weights, rows, need_y=True, need_weights=Tr
     t, top, E = _expert_rows(rows, dev)
     if t != T or tuple(y.shape) != (T * top, K):
         raise ValueError(f"grad must be [{t}, K] and y [{t * top}, K] (got {tuple(grad.shape)} and {tuple(y.shape)})")
+    return _combine_gradients(grad, y, weights, rows.place, rows.offsets, dev, need_y, need_weights)
+
+
+def _combine_gradients(grad, y, weights, place, offsets, dev, need_y, need_weights):
+    """expert_combine_backward of checked arguments; offsets None where dy is not needed."""
+    (T, top), K = place.shape, y.shape[1]
     w, wt = _weights(weights, dev, T, top)
     dy = torch.empty_like(y) if need_y else None
     dw = torch.empty_like(weights) if need_weights and weights is not None else None
+    at, E = (None, 0) if offsets is None else (offsets.data_ptr(), offsets.shape[0] - 1)
     _launch("w4_expert_combine_backward", dev, grad.data_ptr(), _TYPES[grad.dtype], _ptr(y, y.dtype, dev, "y"),
-            _TYPES[y.dtype], w, wt, T, top, K, rows.offsets.data_ptr(), E, rows.place.data_ptr(),
+            _TYPES[y.dtype], w, wt, T, top, K, at, E, place.data_ptr(),
             None if dy is None else dy.data_ptr(), None if dw is None else dw.data_ptr())
     return dy, dw
 
 
-def _take_gradient(grad, rows):
+def _take_gradient(grad, place):
     if grad is None:
         return None
-    return _combine(grad.contiguous(), None, rows, grad.get_device(), None, grad.dtype)
+    return _combine_places(grad.contiguous(), None, place, grad.get_device(), None, grad.dtype)
 
+
+# The gradients keep the indices that they read as saved tensors: autograd refuses a backward pass
+# whose places or offsets were written after the forward pass.
 
 class _TakeFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, rows):
-        ctx.rows = rows
+        xs = _take(x, rows, x.get_device())
+        ctx.save_for_backward(rows.place)
         ctx.set_materialize_grads(False)
-        return _take(x, rows, x.get_device())
+        return xs
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
-        return _take_gradient(grad, ctx.rows), None
+        return _take_gradient(grad, *ctx.saved_tensors), None
 
 
 class _DispatchFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, experts, E):
         xs, rows = _dispatch(x, experts, E)
-        ctx.rows = rows
+        ctx.save_for_backward(rows.place)
         ctx.mark_non_differentiable(*rows)
         ctx.set_materialize_grads(False)
         return (xs,) + rows
@@ -1112,24 +1129,24 @@ class _DispatchFunction(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad, *_):
-        return _take_gradient(grad, ctx.rows), None, None
+        return _take_gradient(grad, *ctx.saved_tensors), None, None
 
 
 class _CombineFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, weights, rows, out_dtype):
-        ctx.save_for_backward(y, weights)
-        ctx.rows = rows
+        out = _combine(y, weights, rows, y.get_device(), None, out_dtype)
+        ctx.save_for_backward(y, weights, rows.place, rows.offsets if ctx.needs_input_grad[0] else None)
         ctx.set_materialize_grads(False)
-        return _combine(y, weights, rows, y.get_device(), None, out_dtype)
+        return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         if grad is None:
             return None, None, None, None
-        y, weights = ctx.saved_tensors
-        return expert_combine_backward(grad.contiguous(), y, weights, ctx.rows, *ctx.needs_input_grad[:2]) + (None, None)
+        return _combine_gradients(grad.contiguous(), *ctx.saved_tensors, grad.get_device(),
+                                  *ctx.needs_input_grad[:2]) + (None, None)
 
 
 def _row_tensor(x, name):

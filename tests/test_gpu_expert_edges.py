@@ -30,3 +30,51 @@ def test_sort_of_runs(w4, gpu, T, top, E):
             got = w4.expert_sort(torch.from_numpy(ids).to(gpu), E)
             for a, b, what in zip(got, want, got._fields):
                 assert np.array_equal(a.cpu().numpy(), b), what
+
+
+def _layer(gpu, T=20, top=2, E=5, K=64, dtype=BF16):
+    """x, ids, y and weights of a small layer, 1/6 of the slots dropped."""
+    rng = np.random.default_rng(31)
+    ids = torch.from_numpy(rng.integers(-1, E, (T, top))).to(gpu)
+    make = lambda *shape: torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).to(gpu)  # noqa: E731
+    return make(T, K).to(dtype), ids, make(T * top, K).to(dtype), make(T, top)
+
+
+def _index_writes(rows):
+    """The tensors of an ExpertRows by name, and what is written into them: other rows, inside their ranges."""
+    return {"place": lambda: rows.place.copy_(rows.place.flip(0)), "offsets": lambda: rows.offsets.fill_(0),
+            "order": lambda: rows.order.fill_(-1)}
+
+
+@pytest.mark.parametrize("call,read", [("dispatch", ["place"]), ("take", ["place"]), ("combine y", ["place", "offsets"]),
+                                       ("combine weights", ["place"]), ("combine sum", ["place", "offsets"])])
+def test_indices_written_before_backward(w4, gpu, call, read):
+    """A gradient whose places or offsets were written since the forward pass is refused; one that does not read
+    what was written is what it was."""
+    x, ids, y, w = _layer(gpu)
+    for name in ("place", "offsets", "order"):
+        _say(f"{call}, {name} written before backward")
+        grads = []
+        for write in (False, True):
+            leaf = {"dispatch": x, "take": x, "combine y": y, "combine weights": w, "combine sum": y}[call]
+            leaf = leaf.clone().requires_grad_()
+            rows = w4.expert_sort(ids, 5)
+            if call == "dispatch":
+                out, rows = w4.expert_dispatch(leaf, ids, 5)
+            elif call == "take":
+                out = w4.expert_take(leaf, rows)
+            elif call == "combine y":
+                out = w4.expert_combine(leaf, w, rows)
+            elif call == "combine weights":
+                out = w4.expert_combine(y, leaf, rows)
+            else:
+                out = w4.expert_combine(leaf, None, rows)
+            if write:
+                _index_writes(rows)[name]()
+            if write and name in read:
+                with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                    out.sum().backward()
+            else:
+                out.sum().backward()
+                grads.append(leaf.grad)
+        assert len(grads) == 1 or torch.equal(*grads)
