@@ -14,6 +14,7 @@ import os
 import typing
 
 import torch
+from torch.autograd import forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libw4.so")
@@ -1149,6 +1150,21 @@ class _CombineFunction(torch.autograd.Function):
                                   *ctx.needs_input_grad[:2]) + (None, None)
 
 
+def _followed(t):
+    """Whether autograd follows what is made of t: in reverse mode, or in forward mode (t is a dual tensor),
+    which the functions above, having no such derivative, refuse."""
+    if not isinstance(t, torch.Tensor):
+        return False
+    if t.requires_grad and torch.is_grad_enabled():
+        return True
+    return _dual_level() >= 0 and forward_ad.unpack_dual(t).tangent is not None
+
+
+def _dual_level():
+    """Below 0 outside forward mode (where asking each tensor would cost 0.3 to 0.7 us)."""
+    return getattr(forward_ad, "_current_level", 0)
+
+
 def _row_tensor(x, name):
     if isinstance(x, torch.Tensor) and x.dim() not in (1, 2):
         raise ValueError(f"{name} must be 1-D or 2-D (got shape {tuple(x.shape)})")
@@ -1157,9 +1173,10 @@ def _row_tensor(x, name):
 
 def expert_take(x, rows, out=None):
     """x [T, K] (or [T]) of bf16, fp32, uint8 or int8 -> its rows in the experts' order, [T * top, K]: row
-    rows.place[t, j] is x[t]; rows of no slot are zeros.  Differentiable (bf16, fp32) without `out`."""
+    rows.place[t, j] is x[t]; rows of no slot are zeros.  Differentiable (bf16, fp32; in reverse mode)
+    without `out`."""
     dev = _row_tensor(x, "x")
-    if out is None and x.requires_grad and torch.is_grad_enabled():
+    if out is None and _followed(x):
         if x.dim() != 2:
             raise ValueError("x must be 2-D for its gradient")
         return _TakeFunction.apply(x, rows)
@@ -1182,9 +1199,9 @@ def _dispatch(x, experts, E):
 
 def expert_dispatch(x, experts, E):
     """expert_sort(experts, E) and expert_take(x, rows) in one call: (xs, ExpertRows).  Differentiable with
-    respect to x (bf16, fp32)."""
+    respect to x (bf16, fp32; in reverse mode)."""
     _row_tensor(x, "x")
-    if x.requires_grad and torch.is_grad_enabled():
+    if _followed(x):
         if x.dim() != 2:
             raise ValueError("x must be 2-D for its gradient")
         xs, *rows = _DispatchFunction.apply(x, experts, E)
@@ -1196,11 +1213,10 @@ def expert_combine(y, weights, rows, out=None, out_dtype=None):
     """The experts' rows y [T * top, K] (bf16, or fp32) brought back to their tokens: out [T, K] = sum over j of
     weights[t, j] * y[rows.place[t, j]], in fp32, of y's type unless `out_dtype` (or `out`) says otherwise.
     weights fp32 or bf16 [T, top], or None for a plain sum.  Dropped slots add nothing, and rows of no slot are
-    not read.  Differentiable with respect to y and weights without `out`."""
+    not read.  Differentiable with respect to y and weights (in reverse mode) without `out`."""
     dev, _, _ = _rows(y, OUT_DTYPES, "y")
     dtype = y.dtype if out_dtype is None else out_dtype
-    if out is None and torch.is_grad_enabled() and (
-            y.requires_grad or (isinstance(weights, torch.Tensor) and weights.requires_grad)):
+    if out is None and (_followed(y) or _followed(weights)):
         return _CombineFunction.apply(y, weights, rows, dtype)
     return _combine(y, weights, rows, dev, out, dtype)
 

@@ -78,3 +78,26 @@ def test_indices_written_before_backward(w4, gpu, call, read):
                 out.sum().backward()
                 grads.append(leaf.grad)
         assert len(grads) == 1 or torch.equal(*grads)
+
+
+def test_forward_mode_is_refused(w4, gpu):
+    """There is no forward-mode derivative of these calls: a dual tensor is refused, and its tangent never dropped;
+    within a dual level plain tensors are taken as ever."""
+    _say("forward mode")
+    x, ids, y, w = _layer(gpu, dtype=F32)
+    rows = w4.expert_sort(ids, 5)
+    plain = [w4.expert_dispatch(x, ids, 5)[0], w4.expert_take(x, rows), w4.expert_take(x[:, 0].contiguous(), rows),
+             w4.expert_combine(y, w, rows), w4.expert_combine(y, None, rows)]
+    with torch.autograd.forward_ad.dual_level():
+        dual = lambda t: torch.autograd.forward_ad.make_dual(t, torch.ones_like(t))  # noqa: E731
+        for call in (lambda: w4.expert_dispatch(dual(x), ids, 5), lambda: w4.expert_take(dual(x), rows),
+                     lambda: w4.expert_combine(dual(y), w, rows), lambda: w4.expert_combine(y, dual(w), rows),
+                     lambda: w4.expert_combine(dual(y), None, rows),
+                     lambda: w4.expert_combine(dual(y.clone().requires_grad_()), w, rows)):
+            for grad in (True, False):
+                with torch.set_grad_enabled(grad), pytest.raises(NotImplementedError, match="jvp|forward"):
+                    call()
+        again = [w4.expert_dispatch(x, ids, 5)[0], w4.expert_take(x, rows), w4.expert_take(x[:, 0].contiguous(), rows),
+                 w4.expert_combine(y, w, rows), w4.expert_combine(y, None, rows)]
+    for a, b in zip(plain, again):
+        assert torch.equal(a, b) and not b.requires_grad
