@@ -1072,37 +1072,41 @@ def _combine_places(y, weights, place, dev, out, out_dtype):
 
 def expert_combine_backward(grad, y, weights, rows, need_y=True, need_weights=True):
     """Gradients of expert_combine for grad [T, K]: (dy [T * top, K] of y's type, zeros in rows of no slot;
-    dweights [T, top] of weights' type, zeros for dropped slots), None where not needed.  (Autograd calls it
-    for an expert_combine whose y or weights require gradients.)"""
+    dweights [T, top] of weights' type, zeros for dropped slots), None where not needed.  (Autograd takes the same
+    entry point for an expert_combine whose y or weights require gradients.)"""
     dev, T, K = _rows(grad, OUT_DTYPES, "grad")
     _, n, _ = _rows(y, OUT_DTYPES, "y")
     t, top, E = _expert_rows(rows, dev)
     if t != T or tuple(y.shape) != (T * top, K):
         raise ValueError(f"grad must be [{t}, K] and y [{t * top}, K] (got {tuple(grad.shape)} and {tuple(y.shape)})")
-    return _combine_gradients(grad, y, weights, rows.place, rows.offsets, dev, need_y, need_weights)
-
-
-def _combine_gradients(grad, y, weights, place, offsets, dev, need_y, need_weights):
-    """expert_combine_backward of checked arguments; offsets None where dy is not needed."""
-    (T, top), K = place.shape, y.shape[1]
     w, wt = _weights(weights, dev, T, top)
-    dy = torch.empty_like(y) if need_y else None
-    dw = torch.empty_like(weights) if need_weights and weights is not None else None
+    return _combine_gradients(grad, _ptr(y, y.dtype, dev, "y"), y.dtype, w, wt, rows.place, rows.offsets, dev,
+                              torch.empty_like(y) if need_y else None,
+                              torch.empty_like(weights) if need_weights and weights is not None else None)
+
+
+def _combine_gradients(grad, y, y_type, weights, weights_type, place, offsets, dev, dy, dw):
+    """Fills dy and dweights (None where not needed) from checked arguments, y and weights by address: dy takes
+    weights and offsets, dweights takes y."""
+    (T, top), K = place.shape, grad.shape[1]
     at, E = (None, 0) if offsets is None else (offsets.data_ptr(), offsets.shape[0] - 1)
-    _launch("w4_expert_combine_backward", dev, grad.data_ptr(), _TYPES[grad.dtype], _ptr(y, y.dtype, dev, "y"),
-            _TYPES[y.dtype], w, wt, T, top, K, at, E, place.data_ptr(),
-            None if dy is None else dy.data_ptr(), None if dw is None else dw.data_ptr())
+    _launch("w4_expert_combine_backward", dev, grad.data_ptr(), _TYPES[grad.dtype], y, _TYPES[y_type], weights,
+            weights_type, T, top, K, at, E, place.data_ptr(), None if dy is None else dy.data_ptr(),
+            None if dw is None else dw.data_ptr())
     return dy, dw
 
 
 def _take_gradient(grad, place):
     if grad is None:
         return None
-    return _combine_places(grad.contiguous(), None, place, grad.get_device(), None, grad.dtype)
+    dev = grad.get_device()
+    _ptr(place, torch.int32, dev, "rows.place")
+    return _combine_places(grad.contiguous(), None, place, dev, None, grad.dtype)
 
 
-# The gradients keep the indices that they read as saved tensors: autograd refuses a backward pass
-# whose places or offsets were written after the forward pass.
+# What the gradients read, indices among it, they keep as saved tensors: autograd refuses a backward
+# pass whose places, offsets or factors were written after the forward pass.  (They are checked again, as
+# a caller's hooks may have replaced them.)
 
 class _TakeFunction(torch.autograd.Function):
     @staticmethod
@@ -1137,7 +1141,11 @@ class _CombineFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, weights, rows, out_dtype):
         out = _combine(y, weights, rows, y.get_device(), None, out_dtype)
-        ctx.save_for_backward(y, weights, rows.place, rows.offsets if ctx.needs_input_grad[0] else None)
+        need_y, need_weights = ctx.needs_input_grad[:2]
+        ctx.types = y.dtype, None if weights is None else weights.dtype
+        # (each gradient reads the other's tensor)
+        ctx.save_for_backward(y if need_weights else None, weights if need_y else None, rows.place,
+                              rows.offsets if need_y else None)
         ctx.set_materialize_grads(False)
         return out
 
@@ -1146,8 +1154,18 @@ class _CombineFunction(torch.autograd.Function):
     def backward(ctx, grad):
         if grad is None:
             return None, None, None, None
-        return _combine_gradients(grad.contiguous(), *ctx.saved_tensors, grad.get_device(),
-                                  *ctx.needs_input_grad[:2]) + (None, None)
+        y, weights, place, offsets = ctx.saved_tensors
+        (need_y, need_weights), (y_type, weights_type) = ctx.needs_input_grad[:2], ctx.types
+        dev, (T, top), K = grad.get_device(), place.shape, grad.shape[1]
+        _ptr(place, torch.int32, dev, "rows.place")
+        if offsets is not None:
+            _ptr(offsets, torch.int32, dev, "rows.offsets")
+        return _combine_gradients(
+            grad.contiguous(), None if y is None else _ptr(y, y_type, dev, "y", (T * top, K)), y_type,
+            None if weights is None else _ptr(weights, weights_type, dev, "weights", (T, top)),
+            _TYPES.get(weights_type, 1), place, offsets, dev,
+            torch.empty((T * top, K), dtype=y_type, device=grad.device) if need_y else None,
+            torch.empty((T, top), dtype=weights_type, device=grad.device) if need_weights else None) + (None, None)
 
 
 def _followed(t):

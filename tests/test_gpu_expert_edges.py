@@ -101,3 +101,66 @@ def test_forward_mode_is_refused(w4, gpu):
                  w4.expert_combine(y, w, rows), w4.expert_combine(y, None, rows)]
     for a, b in zip(plain, again):
         assert torch.equal(a, b) and not b.requires_grad
+
+
+def test_combine_keeps_what_its_gradients_read(w4, gpu):
+    """y is kept for the gradient of the weights only, and the weights for that of y: the other may be freed or
+    written before the backward pass."""
+    x, ids, y, w = _layer(gpu)
+    rows = w4.expert_sort(ids, 5)
+    g = torch.ones_like(x)
+    for weights in (w, None):
+        _say(f"gradient of y alone, weights {weights is not None}")
+        leaf = y.clone().requires_grad_()
+        held = leaf * 2.0
+        out = w4.expert_combine(held, weights, rows)
+        want = w4.expert_combine_backward(g, held.detach(), weights, rows, need_weights=False)[0]
+        with torch.no_grad():
+            held.fill_(float("nan"))
+        out.backward(g)
+        assert torch.equal(leaf.grad, want * 2.0)
+    _say("gradient of the weights alone")
+    leaf = w.clone().requires_grad_()
+    held = leaf * 2.0
+    out = w4.expert_combine(y, held, rows)
+    want = w4.expert_combine_backward(g, y, held.detach(), rows, need_y=False)[1]
+    with torch.no_grad():
+        held.fill_(float("nan"))
+    out.backward(g)
+    assert torch.equal(leaf.grad, want * 2.0)
+    _say("what is read may not be written")
+    for which in ("y", "w"):
+        a, b = y.clone().requires_grad_(), w.clone().requires_grad_()
+        ya, wb = a * 1.0, b * 1.0
+        out = w4.expert_combine(ya, wb, rows)
+        with torch.no_grad():
+            (ya if which == "y" else wb).fill_(1.0)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            out.backward(g)
+    _say("memory held between the passes")
+    T, top, K = 512, 4, 4096
+    big = w4.expert_sort(torch.zeros((T, top), dtype=torch.int64, device=gpu), 1)
+    weights = torch.ones((T, top), device=gpu)
+    leaf = torch.ones((1, K), dtype=BF16, device=gpu).requires_grad_()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated(gpu)
+    out = w4.expert_combine(leaf * torch.ones((T * top, 1), dtype=BF16, device=gpu), weights, big)
+    # (the factor, 2 bytes a row, and out, 2 bytes a value, stay; y, another T * top * K * 2 bytes, does not)
+    assert torch.cuda.memory_allocated(gpu) - before < T * top * K
+    _say("saved tensors that hooks carry away and bring back")
+    x, ids, y, w = _layer(gpu)
+    rows = w4.expert_sort(ids, 5)
+    grads = []
+    for away in (False, True):
+        leaves = [v.clone().requires_grad_() for v in (x, y, w)]
+        with torch.autograd.graph.save_on_cpu() if away else torch.enable_grad():
+            out = (w4.expert_take(leaves[0], rows) + w4.expert_dispatch(leaves[0], ids, 5)[0]).sum() + w4.expert_combine(
+                leaves[1], leaves[2], rows).sum()
+        grads.append(torch.autograd.grad(out, leaves))
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
+    with torch.autograd.graph.saved_tensors_hooks(lambda v: v.cpu(), lambda v: v):
+        out = w4.expert_combine(y.clone().requires_grad_(), w, rows).sum()
+        taken = w4.expert_take(x.clone().requires_grad_(), rows).sum()
+    for loss in (out, taken):
+        with pytest.raises(ValueError, match="several devices"):
+            loss.backward()
