@@ -1009,11 +1009,18 @@ hipError_t launch_product(const MxArgs& a, hipStream_t st) {
     case Mx4::kStream2x4: mx4_stream_kernel<2, 4, false, kF32><<<blocks, 256, 0, st>>>(a); break;
     case Mx4::kStream2x2: mx4_stream_kernel<2, 2, false, kF32><<<blocks, 128, 0, st>>>(a); break;
     case Mx4::kStream2x1: {
-      // Past the caches from 40 MB of weights that the call can read (us through the caches and past
-      // them: one row of 17408 x 5120, 45 MB, 11.2 and 10.5; 8 rows of 8 experts of 9216 x 2560 18.3 and
-      // 16.2; but 2 rows of these 6.2 and 6.9, 16 of 128 of 1408 x 2560, 29 MB, 6.3 and 6.9).
-      const int64_t bytes = (a.experts < a.M ? a.experts : a.M) * (int64_t)a.N * a.K / 2;
-      if (bytes >= (int64_t)40 << 20) mx4_stream_kernel<2, 1, true, kF32><<<blocks, 64, 0, st>>>(a);
+      // Past the caches from 12 MiB of one matrix and from 32 MiB of experts that the call can read (what
+      // the L2s of the eight XCDs hold together).  Us through the caches and past them, one row: 16384 x
+      // 1408 (11 MiB) 4.53 and 4.75, 65536 x 384 (12 MiB) 6.06 and 5.68, 28672 x 1408 (19 MiB) 6.72 and
+      // 6.19, 28672 x 5120 (70 MiB) 15.8 and 14.2; 16 rows 4.90 and 5.15, 6.74 and 6.56, 7.14 and 6.70, 17.2
+      // and 16.1.  Experts drawn at random: 4 rows of 32 of 2560 x 4096 (20 MiB) 6.60 and 7.67, 32 of 256 of
+      // 2048 x 896 (28 MiB) 8.24 and 8.38, 24 of 64 of 1408 x 2048 (33 MiB) 8.73 and 8.04, 16 of 64 of 2048 x
+      // 2560 (40 MiB) 9.75 and 9.05, 16 of 32 of 2560 x 4096 (80 MiB) 17.9 and 16.2.  Between 16 and 32 MiB
+      // either may win, by 7% at most below 32 (16 of 64 of 2048 x 1408, 22 MiB: 7.05 and 6.64); where one
+      // expert has all the rows, past them takes up to 13% longer (14 rows of one of 32: 6.1 and 6.9).
+      const int64_t busy = a.experts < a.M ? a.experts : a.M, bytes = busy * a.N * a.K / 2;
+      if (bytes >= (busy == 1 ? 12 : 32) * (int64_t(1) << 20))
+        mx4_stream_kernel<2, 1, true, kF32><<<blocks, 64, 0, st>>>(a);
       else mx4_stream_kernel<2, 1, false, kF32><<<blocks, 64, 0, st>>>(a);
       break;
     }
