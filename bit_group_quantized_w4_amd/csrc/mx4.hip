@@ -924,21 +924,32 @@ enum class Mx4 { kTile256, kDeep128, kDeep64x128, kDeep64, kDeep32x64, kStream1x
 struct Mx4Shape {
   Mx4 kind;
   int BM, BN, threads;
-  // the estimate of a call's time, us: start + (steps of 256 inputs) * max(one, all * blocks / slots)
+  // the estimate of a call's time, us: start + (steps of 256 inputs) * max(one, all * blocks / slots),
+  // and no less than bare + steps * step, what few blocks take
   int slots;
-  double start, one, all;
+  double start, one, all, bare, step;
 };
 // Constants that lose least by the choice over the times of all these kernels (other weights than
 // the last call's) on 14 matrices, N from 300 to 28672 and K from 128 to 9216, at 17 to 3000 rows and on 5
-// sets of 8 to 128 experts at 13 to 400 rows each, popularity as 1 / rank and its root: 2.5% on
+// sets of 8 to 128 experts at 13 to 400 rows each, popularity as 1 / rank and its root: 2.6% on
 // average against the best of them each time, 32% at most.  (Constants fitted to one half of the
 // sizes lose 2.6 to 3.5% on the other, and so do rounds of blocks counted as whole.)
+// Two of them fit with `one` at zero, which says nothing of few outputs and many inputs: for these
+// bare and step, from the times of launches of few blocks.  On 15 more matrices, N from 33 to 8192 and
+// K from 9216 to 130944, and 3 sets of experts, the choice loses 3.6% on average and 53% at most (32%
+// and 168% without bare and step: 64 rows of 2048 x 28672 took 60.4 us as 64 x 128, and take 22.5
+// streamed); on 240 sizes drawn from N of 16 to 28672, K of 128 to 28672 and up to 128 experts 4.4%
+// and 75% (4060 rows of 54 experts of 25 x 15360, streamed 24.4 us, as 32 x 64 13.9).
 constexpr Mx4Shape kMx4Shapes[] = {
-    {Mx4::kTile256, 256, 256, 512, 256, 3.4, 0, 1.77},    {Mx4::kDeep128, 128, 128, 256, 256, 6.2, 0.473, 0.669},
-    {Mx4::kDeep64x128, 64, 128, 256, 256, 9.7, 0, 0.395}, {Mx4::kDeep64, 64, 64, 256, 512, 3.7, 0.227, 0.669},
-    {Mx4::kDeep32x64, 32, 64, 128, 512, 3.6, 0.2, 0.547}, {Mx4::kStream2x2, 16, 32, 128, 2048, 3.8, 0, 1.33},
-    {Mx4::kStream2x1, 16, 32, 64, 4096, 2.7, 0.343, 1.53}, {Mx4::kStream2x4, 16, 32, 256, 0, 0, 0, 0},
-    {Mx4::kStream1x4, 16, 16, 256, 0, 0, 0, 0},
+    {Mx4::kTile256, 256, 256, 512, 256, 3.4, 0, 1.77, 0, 0},
+    {Mx4::kDeep128, 128, 128, 256, 256, 6.2, 0.473, 0.669, 0, 0},
+    {Mx4::kDeep64x128, 64, 128, 256, 256, 9.7, 0, 0.395, 4.1, 0.295},
+    {Mx4::kDeep64, 64, 64, 256, 512, 3.7, 0.227, 0.669, 0, 0},
+    {Mx4::kDeep32x64, 32, 64, 128, 512, 3.6, 0.2, 0.547, 0, 0},
+    {Mx4::kStream2x2, 16, 32, 128, 2048, 3.8, 0, 1.33, 3.4, 0.125},
+    {Mx4::kStream2x1, 16, 32, 64, 4096, 2.7, 0.343, 1.53, 0, 0},
+    {Mx4::kStream2x4, 16, 32, 256, 0, 0, 0, 0, 0, 0},
+    {Mx4::kStream1x4, 16, 16, 256, 0, 0, 0, 0, 0, 0},
 };
 
 // The kernel for M rows shared out over `experts` matrices of N x K (their true sizes are on
@@ -966,7 +977,8 @@ Mx4 choose_mx4(int64_t M, int64_t N, int64_t K, int64_t experts) {
       const int64_t left = blocks % kCus;
       load = (double)(blocks / kCus) + (left == 0 ? 0 : left <= kMostCut ? 0.45 : 1);
     }
-    const double cost = s.start + (double)steps * (load * s.all > s.one ? load * s.all : s.one);
+    const double full = s.start + (double)steps * (load * s.all > s.one ? load * s.all : s.one);
+    const double few = s.bare + (double)steps * s.step, cost = full > few ? full : few;
     if (least == 0 || cost < least) {
       least = cost;
       best = s.kind;

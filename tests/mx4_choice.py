@@ -15,7 +15,8 @@ REPEATED = [
     "const int64_t spread = M / s.BM + busy / 2; const int64_t tiles = busy == 1 ? (M + s.BM - 1) / s.BM : spread > busy ? "
     "spread : busy; const int64_t blocks = tiles * ((N + s.BN - 1) / s.BN); double load = (double)blocks / s.slots;",
     "load = (double)(blocks / kCus) + (left == 0 ? 0 : left <= kMostCut ? 0.45 : 1);",
-    "const double cost = s.start + (double)steps * (load * s.all > s.one ? load * s.all : s.one);",
+    "const double full = s.start + (double)steps * (load * s.all > s.one ? load * s.all : s.one); const double few = s.bare + "
+    "(double)steps * s.step, cost = full > few ? full : few;",
     "constexpr int kCus = 256, kMostCut = kCus / 4;",
     "const int64_t busy = a.experts < a.M ? a.experts : a.M, bytes = busy * a.N * a.K / 2; if (bytes >= (busy == 1 ? 12 : 32) * "
     "(int64_t(1) << 20))",
@@ -28,8 +29,8 @@ def source():
 
 
 def shapes():
-    """(kind, BM, BN, threads, slots, start, one, all) of the estimate's kernels."""
-    found = re.findall(r"\{Mx4::k(\w+), (\d+), (\d+), (\d+), (\d+), ([\d.]+), ([\d.]+), ([\d.]+)\}", source())
+    """(kind, BM, BN, threads, slots, start, one, all, bare, step) of the estimate's kernels."""
+    found = re.findall(r"\{Mx4::k(\w+)" + r", (\d+)" * 4 + r", ([\d.]+)" * 5 + r"\}", source())
     return [(f[0], *map(int, f[1:5]), *map(float, f[5:])) for f in found]
 
 
@@ -45,7 +46,7 @@ def kernel(M, N, K, experts=1):
         best = "Stream1x4" if nb < 256 else "Stream2x4" if nb < 384 else "Stream2x2" if nb < 1024 else "Stream2x1"
     else:
         least = None
-        for kind, BM, BN, _, slots, start, one, every in shapes():
+        for kind, BM, BN, _, slots, start, one, every, bare, step in shapes():
             if not slots:
                 continue
             tiles = up(M, BM) if busy == 1 else max(M // BM + busy // 2, busy)
@@ -54,7 +55,7 @@ def kernel(M, N, K, experts=1):
             if kind == "Tile256":
                 left = blocks % 256
                 load = blocks // 256 + (0 if left == 0 else 0.45 if left <= 64 else 1)
-            cost = start + steps * max(load * every, one)
+            cost = max(start + steps * max(load * every, one), bare + steps * step)
             if least is None or cost < least:
                 least, best = cost, kind
     if best == "Stream2x1" and busy * N * K // 2 >= (12 if busy == 1 else 32) * MiB:
@@ -72,7 +73,7 @@ DENSE = {
     "Stream2x1Past": [(1, 65537, 384), (16, 28673, 1152), (20, 65537, 384), (17, 30001, 896)],
     "Deep32x64": [(19, 4555, 1664), (154, 1133, 4224)],
     "Deep64": [(251, 1774, 5248), (311, 8545, 128)],
-    "Deep64x128": [(500, 2561, 9088), (153, 983, 9856), (37, 3132, 9856)],
+    "Deep64x128": [(500, 2561, 9088), (263, 3140, 11392)],
     "Deep128": [(327, 8264, 1152), (273, 7413, 2816)],
     "Tile256": [(260, 7521, 128), (633, 4908, 2176)],
 }
@@ -84,7 +85,7 @@ GROUPED = {
     "Stream2x1Past": [([3, 0, 16, 1, 9, 17, 40, 0, 2, 5, 1, 7], 2561, 2432), ([20, 0, 16, 52, 30, 2], 4867, 3456)],
     "Deep32x64": [([20, 2, 49, 0, 72], 1130, 5248)],
     "Deep64": [([130, 0, 1, 100, 66], 1547, 5376)],
-    "Deep64x128": [([140, 0, 5], 1098, 9984), ([100, 0, 70, 33, 12, 130, 56], 342, 9984)],
+    "Deep64x128": [([433, 0, 458], 1746, 6784), ([200, 0, 170, 233, 264], 1352, 8576)],
     "Deep128": [([70, 128, 0, 131, 11, 123], 3703, 2176)],
     "Tile256": [([257, 0, 300, 15], 3481, 128)],
 }

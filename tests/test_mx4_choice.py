@@ -33,3 +33,13 @@ def test_the_kernels_of_some_sizes():
     """Sizes of tests that say otherwise beside them: few outputs and few steps are streamed."""
     assert mx4_choice.kernel(64, 5000, 1408) == mx4_choice.kernel(333, 3000, 384) == "Stream2x1"
     assert mx4_choice.kernel(512, 2560, 9216) == "Deep64x128"
+
+
+def test_few_blocks_take_their_steps():
+    """No kernel's estimate leaves out the steps of a launch of few blocks, and few outputs of many inputs are not given
+    to the larger tiles (us as 64 x 128 and streamed by two and two: 37.8 and 18.8, 60.4 and 22.5, 35.0 and 18.3)."""
+    for kind, _, _, _, slots, start, one, every, bare, step in mx4_choice.shapes():
+        # (256 x 256: half a round of tiles is the least there is)
+        assert not slots or max(one, step, 0.45 * every if kind == "Tile256" else 0) > 0, kind
+    for M, N, K in ((512, 256, 28672), (64, 2048, 28672), (100, 1024, 28672)):
+        assert mx4_choice.kernel(M, N, K) == "Stream2x2", (M, N, K)
