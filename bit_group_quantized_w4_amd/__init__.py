@@ -1001,9 +1001,8 @@ def _empty_rows(T, top, E, device):
     """(ExpertRows to be filled, address of a workspace or None, its bytes, what holds it)."""
     nb = _sort_bytes(T, top, E)
     # (buffers of their own, not parts of one: autograd counts the writes of each by itself)
-    rows = ExpertRows(torch.empty(E + 1, dtype=torch.int32, device=device),
-                      torch.empty((T, top), dtype=torch.int32, device=device),
-                      torch.empty(T * top, dtype=torch.int32, device=device))
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=device)
+    rows = ExpertRows(offsets, offsets.new_empty((T, top)), offsets.new_empty(T * top))
     if not nb:
         return rows, None, 0, None
     work = torch.empty(nb, dtype=torch.uint8, device=device)
@@ -1081,18 +1080,17 @@ def expert_combine_backward(grad, y, weights, rows, need_y=True, need_weights=Tr
         raise ValueError(f"grad must be [{t}, K] and y [{t * top}, K] (got {tuple(grad.shape)} and {tuple(y.shape)})")
     w, wt = _weights(weights, dev, T, top)
     return _combine_gradients(grad, _ptr(y, y.dtype, dev, "y"), y.dtype, w, wt, rows.place, rows.offsets, dev,
-                              torch.empty_like(y) if need_y else None,
+                              (T, top, K, E), torch.empty_like(y) if need_y else None,
                               torch.empty_like(weights) if need_weights and weights is not None else None)
 
 
-def _combine_gradients(grad, y, y_type, weights, weights_type, place, offsets, dev, dy, dw):
+def _combine_gradients(grad, y, y_type, weights, weights_type, place, offsets, dev, sizes, dy, dw):
     """Fills dy and dweights (None where not needed) from checked arguments, y and weights by address: dy takes
     weights and offsets, dweights takes y."""
-    (T, top), K = place.shape, grad.shape[1]
-    at, E = (None, 0) if offsets is None else (offsets.data_ptr(), offsets.shape[0] - 1)
+    T, top, K, E = sizes
     _launch("w4_expert_combine_backward", dev, grad.data_ptr(), _TYPES[grad.dtype], y, _TYPES[y_type], weights,
-            weights_type, T, top, K, at, E, place.data_ptr(), None if dy is None else dy.data_ptr(),
-            None if dw is None else dw.data_ptr())
+            weights_type, T, top, K, None if offsets is None else offsets.data_ptr(), E, place.data_ptr(),
+            None if dy is None else dy.data_ptr(), None if dw is None else dw.data_ptr())
     return dy, dw
 
 
@@ -1158,29 +1156,25 @@ class _CombineFunction(torch.autograd.Function):
         (need_y, need_weights), (y_type, weights_type) = ctx.needs_input_grad[:2], ctx.types
         dev, (T, top), K = grad.get_device(), place.shape, grad.shape[1]
         _ptr(place, torch.int32, dev, "rows.place")
+        E = 0 if offsets is None else _experts(offsets)
         if offsets is not None:
             _ptr(offsets, torch.int32, dev, "rows.offsets")
         return _combine_gradients(
             grad.contiguous(), None if y is None else _ptr(y, y_type, dev, "y", (T * top, K)), y_type,
             None if weights is None else _ptr(weights, weights_type, dev, "weights", (T, top)),
-            _TYPES.get(weights_type, 1), place, offsets, dev,
+            _TYPES.get(weights_type, 1), place, offsets, dev, (T, top, K, E),
             torch.empty((T * top, K), dtype=y_type, device=grad.device) if need_y else None,
             torch.empty((T, top), dtype=weights_type, device=grad.device) if need_weights else None) + (None, None)
 
 
-def _followed(t):
-    """Whether autograd follows what is made of t: in reverse mode, or in forward mode (t is a dual tensor),
-    which the functions above, having no such derivative, refuse."""
-    if not isinstance(t, torch.Tensor):
-        return False
-    if t.requires_grad and torch.is_grad_enabled():
+def _followed(t, u=None):
+    """Whether autograd follows what is made of tensors t and (perhaps) u: in reverse mode, or in forward mode
+    (one is a dual tensor), which the functions above, having no such derivative, refuse."""
+    if torch.is_grad_enabled() and (t.requires_grad or (isinstance(u, torch.Tensor) and u.requires_grad)):
         return True
-    return _dual_level() >= 0 and forward_ad.unpack_dual(t).tangent is not None
-
-
-def _dual_level():
-    """Below 0 outside forward mode (where asking each tensor would cost 0.3 to 0.7 us)."""
-    return getattr(forward_ad, "_current_level", 0)
+    # (the level is below 0 outside forward mode, where asking each tensor would cost 0.3 to 0.7 us)
+    return getattr(forward_ad, "_current_level", 0) >= 0 and any(
+        isinstance(v, torch.Tensor) and forward_ad.unpack_dual(v).tangent is not None for v in (t, u))
 
 
 def _row_tensor(x, name):
@@ -1234,7 +1228,7 @@ def expert_combine(y, weights, rows, out=None, out_dtype=None):
     not read.  Differentiable with respect to y and weights (in reverse mode) without `out`."""
     dev, _, _ = _rows(y, OUT_DTYPES, "y")
     dtype = y.dtype if out_dtype is None else out_dtype
-    if out is None and (_followed(y) or _followed(weights)):
+    if out is None and _followed(y, weights):
         return _CombineFunction.apply(y, weights, rows, dtype)
     return _combine(y, weights, rows, dev, out, dtype)
 
