@@ -404,7 +404,12 @@ __global__ __launch_bounds__(256) void expert_combine_kernel(const CombineArgs a
       for (int e = 0; e < V; ++e) s[e] = fmaf(w[j], f[e], s[e]);
     }
   }
-  store_values<true>(a.out, a.out_f32, t * a.K + at, s);  // past the caches: 71 and 59 us (4095 x 8 rows of 5120)
+  // Past the caches at every length: rows of out follow each other, so that those which end inside a
+  // line gain too (us through the caches and past them: 4095 x 8 rows of 5120 bf16 74.6 and 69.8, of 5121
+  // 75.1 and 71.5, fp32 146.6 and 139.7; 20000 x 6 of 700 41.6 and 38.8; 16384 x 2 of 1027 28.9 and 27.7; 32767 x
+  // 2 of 257 19.8 and 17.9).  Calls of 5 us or less with such rows take 0.2 us longer (8 x 2 of 2561 3.6 and
+  // 3.8; of 512 x 2 of 2560, whole lines, 4.7 and 4.6).
+  store_values<true>(a.out, a.out_f32, t * a.K + at, s);
 }
 
 // The gradients: W wavefronts of a block, or (W = 0) `lanes` lanes of a wavefront, have a
@@ -617,8 +622,11 @@ hipError_t launch_expert_combine(const CombineArgs& a, hipStream_t st) {
 hipError_t launch_expert_combine_backward(const CombineBackwardArgs& a, hipStream_t st) {
   const int64_t per = a.y_f32 ? 4 : 8, tokens = a.slots / a.top;
   const Lanes l = lanes_of(a.K < per ? a.K : (a.K + per - 1) / per);
-  // A block per token while there are few (us, 512 tokens x 2 rows of 2560: 7.6, and 10.9 with a
-  // wavefront each; 4095 x 8 rows of 5120 154 and 143).
+  // A block per token while there are few (us by block and by wavefront, 512, 1023, 1500 and 2048 tokens:
+  // x 2 rows of 2560 9.3 and 14.2, 12.1 and 15.1, 19.7 and 17.8, 23.0 and 18.9; x 8 rows of 2560 16.6 and 26.1, 24.8 and
+  // 30.2, 41.0 and 40.7, 47.7 and 44.7; x 8 rows of 700 9.0 and 12.1, 11.2 and 13.2, 18.1 and 15.5, 20.6 and 16.8; x 1
+  // row of 1024 6.3 and 6.9, 8.0 and 8.0, 12.4 and 8.9, 14.7 and 9.2; rows of 5120 gain up to 2048: x 8 40.1 and 54.8,
+  // 66.2 and 77.5, 79.3 and 83.4 from 1023 on; 4095 x 8 152 and 140).
   const bool past = a.dy && a.dw ? whole_lines(a.dy, a.K * (a.y_f32 ? 4 : 2)) && whole_lines(a.y, a.K * (a.y_f32 ? 4 : 2))
                                  : whole_lines(a.dy, a.K * (a.y_f32 ? 4 : 2));
   auto go = [&](auto w4, auto w1, auto w0) {

@@ -278,6 +278,9 @@ __global__ __launch_bounds__(256) void dequantize_weights_kernel(const uint8_t* 
 
 // Codes [N][K / 2] and scales [N][K / 32] row-major <-> native: a thread has one lane of
 // a row block's 512 inputs, up to four blocks and their word of scales.
+//
+// Bound by its requests, 16 bytes of 16 rows per load and a byte of scales per lane: 28672 x 8192 (250 MB)
+// takes 59 us packed and 65 unpacked (4.2 and 3.8 TB/s), 9216 x 2560 8.1 and 7.8.
 template <bool kPack>
 __global__ __launch_bounds__(256) void repack_mx4_kernel(uint8_t* __restrict__ canon, uint8_t* __restrict__ canon_scales,
                                                          int64_t N, int K, int words, int64_t items,
@@ -357,9 +360,9 @@ __device__ __forceinline__ Operands operands_of(const MxArgs& a, const RowTile& 
 // a row block, inputs 64 (l / 16) .. + 63 of 256, and D[4 (l / 16) + j][l % 16], j = 0..3,
 // all straight from memory, D pairs of tiles ahead of the products.
 //
-// Bound by the weight stream: 13 rows of 28672 x 8192 (125 MB) take 22 us (5.8 TB/s); one row of
+// Bound by the weight stream: 13 rows of 28672 x 8192 (125 MB) take 22.3 us (5.6 TB/s); one row of
 // 9216 x 2560 4.8 us, the latency of its loads and of the join over K.  (Three or four pairs ahead
-// leave fewer wavefronts room: 24.0 and 24.2 us.)
+// leave fewer wavefronts room: 23.2 and 23.5 us.)
 template <int R, int NW, int kCache, bool kF32>
 __device__ __forceinline__ void stream_row_tile(const MxArgs& a, const RowTile& rt, int rb0, f32x4 (&red)[NW][R][64]) {
   constexpr int D = 2;
@@ -440,7 +443,7 @@ __device__ __forceinline__ void stream_row_tile(const MxArgs& a, const RowTile& 
 }
 
 // kPast: an expert's weights are read past the caches, unless another row tile of the
-// expert reads them too (13 rows of 28672 x 8192 24.6 us past them, 26.8 through them).
+// expert reads them too (13 rows of 28672 x 8192 22.3 us past them, 23.7 through them).
 template <int R, int NW, bool kPast, bool kF32>
 __global__ __launch_bounds__(NW * 64) void mx4_stream_kernel(const MxArgs a) {
   const int nb = (a.N + kTileRows - 1) / kTileRows, panels = (nb + R - 1) / R;
@@ -796,12 +799,13 @@ __global__ __launch_bounds__(512, 1) void mx4_tile_kernel(const MxArgs a, int pa
 
 // Fewer rows: smaller tiles, four buffers, loads three steps ahead, two parts (one product each)
 // per step; a load is issued behind a product, which runs meanwhile (64 rows of 2561 x 9216 9.4 us ahead
-// of the products, 8.9 behind).  333 rows of 2561 x 9216 take 11.2 us as 64 x 64 (37 streamed, 19 as 128 x 128 of
-// this form, 33 as 256 x 256).
+// of the products, 8.9 behind).  333 rows of 2561 x 9216 take 12.0 us as 64 x 64 (36.7 streamed, 14.8 as 64 x
+// 128, 19.8 as 128 x 128 of this form, 32 as 256 x 256).  (Eight matrices in turn; forty, whose codes come from
+// memory: 12.6 us for the 64 rows, 13.8 for the 333.)
 //
-// Bound by the rate at which a CU loads into LDS, 18 KB of a step in 0.2 us: the loads alone, without
-// products and reads of LDS, take 11.0 of the 11.2 us; the rest alone 8.1, an empty loop 4.0; 41 blocks
-// (64 rows) take no less than 246.  Six or eight buffers change nothing (11.5 and 12.8, with the steps past the
+// Bound by the rate at which a CU loads into LDS, 18 KB of a step in 0.2 us: on the card where 333 rows take
+// 11.2 us, the loads alone, without products and reads of LDS, take 11.0; the rest alone 8.1, an empty loop
+// 4.0; 41 blocks (64 rows) take no less than 246.  Six or eight buffers change nothing (11.5 and 12.8, with the steps past the
 // last); two 20 us.  (Two wavefronts for each tile twice as high, one product of a step each, read
 // 24 KB of LDS instead of 40, and take 11.9 with the join; groups of wavefronts that divide the steps 13;
 // operands straight to registers, K divided among the wavefronts, 20.)
@@ -955,11 +959,15 @@ constexpr Mx4Shape kMx4Shapes[] = {
 // The kernel for M rows shared out over `experts` matrices of N x K (their true sizes are on
 // the GPU).  Up to 16 rows each the
 // streaming form with as many wavefronts as there are few outputs (us, one row: 2560 x 9216 as
-// one row block and four wavefronts 4.6, as two and four 5.1, two and two 6.1, two and
-// one 13; 5120 x 5120 5.5, 4.8, 4.7, 8.3; 9216 x 2560 5.3, 5.5, 4.8, 5.5; 13 rows of 28672 x 8192
-// 32.4, 29.0, 26.8, 23.1).  Beyond that the smallest estimate.  512 rows: 2560 x 9216 take 14.6 us as
-// 64 x 128 (160 blocks), 18.4 as 64 x 64, 19.1 as 128 x 128 and 31 as 256 x 256 (20 blocks);
-// 17408 x 5120 45, 47, 40 and 35 us.
+// one row block and four wavefronts 4.9, as two and four 5.4, two and two 6.3, two and
+// one 10; 5120 x 5120 6.4, 5.5, 6.0, 8.6; 9216 x 2560 5.7, 5.9, 5.2, 5.5; 13 rows of 28672 x 8192
+// 31, 28.5, 25.8, 23.7.  Experts drawn at random: 2 rows of 64 of 2048 x 2560 (nb 256) 3.9, 4.1, 4.0, 4.7; 4
+// rows 4.9, 4.7, 4.4, 4.9; 16 rows 13.3, 11.5, 11.0, 9.1; 8 rows of 128 of 1408 x 2560 (nb 704) 5.9, 6.0, 5.5,
+// 5.4; of 256 of 2048 x 896 (nb 1024) 5.9, 5.0, 4.3, 4.4; no such call of 8 sets of experts gained more than 4%
+// by another of the four).  An expert that has all rows is streamed 16 at a time all the same: 512 rows of
+// one of 64 of 2048 x 2560 13.6 us, as 64 x 64 7.4.  Beyond that the smallest estimate.  512 rows: 2560 x 9216
+// take 14.6 us as 64 x 128 (160 blocks), 18.3 as 64 x 64, 19.2 as 128 x 128 and 31 as 256 x 256 (20 blocks);
+// 17408 x 5120 (codes from memory) 59, 58, 50, which the estimate takes, and 41.
 Mx4 choose_mx4(int64_t M, int64_t N, int64_t K, int64_t experts) {
   const int64_t busy = experts < M ? experts : M, rows = (M + busy - 1) / busy;
   const int64_t nb = (N + kTileRows - 1) / kTileRows * busy, steps = (K + kPair - 1) / kPair;
